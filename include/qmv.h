@@ -415,6 +415,154 @@ int qmv_quantize_fp(const void* w, void* w_packed, void* scales, const float* gl
                     int mode, int dtype, void* stream);
 
 /*
+ * Between the Q / K / V projection and the output projection
+ * -----------------------------------------------------------------
+ * qmv_affine_qkv leaves [Q | K | V] rows; the three calls below rotate the
+ * heads by their positions, store keys and values in a paged cache, and attend
+ * over it.  The pages list these operators beside the quantized products
+ * (wh-iron kernel-op coverage audit: rope and sdpa rows) and give no
+ * formulas; the ones used are written out here.  All three serve one new
+ * token per sequence and long chunks of new tokens alike, launch on `stream`
+ * with programmatic dependent launch (reading nothing before the kernel before
+ * them has finished), allocate nothing, and can be captured into a graph.
+ */
+#define QMV_MAX_HEAD_DIM 256
+
+/* How a head's first rot_dim dims pair up: pair i is (i, i + rot_dim / 2) or
+ * (2 i, 2 i + 1). */
+typedef enum { QMV_ROPE_HALF = 0, QMV_ROPE_INTERLEAVED = 1 } qmv_rope_layout;
+
+/* Frequencies of qmv_rope_frequencies: f_i = base^(-2 i / rot_dim), then
+ *   LINEAR  f_i / factor (positions squeezed into the trained length);
+ *   BASE    base multiplied by factor^(rot_dim / (rot_dim - 2)), so that the
+ *           slowest pair is stretched by factor and the fastest is kept;
+ *   BANDED  pairs that make more than turns_fast turns over original_length
+ *           are kept, those below turns_slow divided by factor, blended
+ *           linearly in i between; magnitude 0.1 ln(factor) + 1 (Peng et al.
+ *           2023, "YaRN"). */
+typedef enum { QMV_ROPE_PLAIN = 0, QMV_ROPE_LINEAR = 1, QMV_ROPE_BASE = 2, QMV_ROPE_BANDED = 3 } qmv_rope_scaling;
+
+/*
+ * qmv_rope_frequencies -- HOST helper: writes rot_dim / 2 floats to inv_freq
+ * and the magnitude (1 except for BANDED) to *magnitude, both HOST pointers,
+ * computed in double and rounded once.  base > 1, rot_dim even and >= 2;
+ * factor >= 1 unless PLAIN; BASE needs rot_dim > 2; BANDED needs
+ * original_length >= 1 and turns_fast > turns_slow > 0 (32 and 1 are usual).
+ * Arguments that a scaling does not use are ignored.
+ */
+int qmv_rope_frequencies(float* inv_freq, float* magnitude, int rot_dim, double base, int scaling, double factor,
+                         int original_length, double turns_fast, double turns_slow);
+
+/*
+ * qmv_rope -- rotary positions: y = x with pair i of every head of token t
+ * turned by the angle a = positions[t] * inv_freq[i]:
+ *     (u, w) -> magnitude * (u cos a - w sin a, u sin a + w cos a)
+ * and dims rot_dim..D-1 copied.  The rotation by -positions undoes it and is its
+ * gradient (magnitude 1).
+ *   x, y      [T, H, D] dtype, element (t, h, d) at t * token_stride +
+ *             h * head_stride + d (strides in elements; x's may be 0).  y may
+ *             be x with the same strides; otherwise the spans of memory from
+ *             their first to their last element must not meet (QMV_EINVAL).
+ *   positions [T] int32, any sign; inv_freq [rot_dim / 2] float (device)
+ *   1 <= D <= QMV_MAX_HEAD_DIM; rot_dim even, 2 <= rot_dim <= D; layout a
+ *   qmv_rope_layout.  T == 0 or H == 0 is a no-op.
+ * The angle is formed and reduced in fp64, the rotation in fp32, rounded once.
+ * 16-byte aligned rows are moved 16 bytes at a time (8, 4, element otherwise).
+ */
+int qmv_rope(const void* x, void* y, const int* positions, const float* inv_freq, int T, int H, int D, int rot_dim,
+             int layout, float magnitude, long long x_token_stride, long long x_head_stride, long long y_token_stride,
+             long long y_head_stride, int dtype, void* stream);
+
+/*
+ * A paged cache of keys and values and the batch that is run on it (a host
+ * struct of device pointers, read during the call).
+ *   k, v         element (page, row, head, d) at page * page_stride +
+ *                row * token_stride + head * head_stride + d, in elements, d
+ *                contiguous: [pages, rows, heads, D] and [pages, heads, rows,
+ *                D] both fit.  Rows of the cache must not overlap.
+ *   page_table   [n_seqs, max_pages] int32: page of positions
+ *                e * page_size .. of sequence b at [b, e]
+ *   q_starts     [n_seqs + 1] int32, ascending: sequence b's new tokens are
+ *                rows q_starts[b] .. q_starts[b + 1] - 1 of the call's T rows
+ *                (none is allowed); rows before the first and behind the last
+ *                sequence are not read and their outputs not written
+ *   kv_lens      [n_seqs] int32: keys of sequence b, its new tokens included;
+ *                new token i is at position kv_lens[b] - n_new + i
+ * The lists live on the device, so the host cannot check them.  Wrong entries
+ * never lead a kernel outside the arrays: see each call.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    long long page_stride, token_stride, head_stride;
+    int n_pages, page_size, n_kv_heads, head_dim, dtype;
+    int n_seqs, max_pages;
+    const int* page_table;
+    const int* q_starts;
+    const int* kv_lens;
+} qmv_paged_kv;
+
+/*
+ * qmv_kv_append -- rotate and store: one launch that takes the rows that
+ * qmv_affine_qkv writes, rotates their query heads to q_out and their key
+ * heads into the cache, and copies their value heads into the cache.
+ *   qkv       row t at t * qkv_stride elements: n_q_heads query heads, then
+ *             n_kv_heads key heads, then n_kv_heads value heads of head_dim
+ *             (qkv_stride >= their total)
+ *   q_out     [T, n_q_heads, head_dim], row t at t * q_out_stride; NULL leaves
+ *             the queries alone (n_q_heads may be 0 then).  It may be qkv
+ *             itself with the same stride; otherwise the two spans of memory
+ *             must not meet (QMV_EINVAL).
+ *   positions [T] int32 angles' positions, or NULL: the position in the
+ *             sequence.  Where a row is stored never depends on it.
+ *   inv_freq, rot_dim, layout, magnitude as for qmv_rope; inv_freq NULL: no
+ *             rotation (the others ignored)
+ * A token whose position is negative, or whose page lies outside the table
+ * (>= max_pages) or the cache (id outside [0, n_pages)), is not stored; its
+ * queries are rotated.  Two tokens that share a place of the cache race.
+ */
+int qmv_kv_append(const void* qkv, long long qkv_stride, const qmv_paged_kv* kv, const int* positions,
+                  const float* inv_freq, void* q_out, long long q_out_stride, int T, int n_q_heads, int rot_dim,
+                  int layout, float magnitude, void* stream);
+
+/*
+ * qmv_paged_attention -- attention of the new tokens over the cache (their own
+ * keys are in it).  Query head h uses kv head h / (n_q_heads / n_kv_heads).
+ * For the token at position p and a key at position j < kv_lens[b]:
+ *     s = scale * q . k;  softcap > 0: s = softcap * tanh(s / softcap);
+ *     slopes: s += slopes[h] * (j - p)
+ *   causal = 1: only keys j <= p;  window > 0: only keys j > p - window
+ *     out = sum_j softmax(s)_j v_j,   lse = log sum_j exp(s_j)
+ * A row that sees no key, or whose scores are all -infinity, gives out = 0
+ * and lse = -infinity.  Keys and values a row does not see never reach it,
+ * whatever they hold.  A key that lies on a bad page (see qmv_kv_append) makes
+ * the rows that see it NaN.
+ *   q, out    [T, n_q_heads, head_dim] dtype of the cache, by token and head
+ *             strides (elements; q's may be 0); out must not overlap q or the cache
+ *   lse       [T, n_q_heads] float, or NULL
+ *   slopes    [n_q_heads] float (device), or NULL
+ *   scale > 0; softcap >= 0; window >= 0; n_q_heads a multiple of n_kv_heads
+ *   max_q_len the most new tokens of a sequence, 0 if not known: only chooses
+ *             the kernel, the result does not depend on it
+ *   workspace NULL, or a device buffer of QMV_PAGED_ATTENTION_WORKSPACE_BYTES,
+ *             16-byte aligned, ALL ZERO before its first use (cudaMemset
+ *             once); every call leaves it ready for the next, of any sizes.
+ *             With it the keys of a sequence are shared out over blocks
+ *             (which the sums' order depends on, so results without it may
+ *             differ by rounding; with the same arguments they do not).
+ *             Calls that share a workspace must not overlap on the GPU.
+ * Scores, softmax statistics and sums are fp32; out is rounded once.  For f16
+ * and bf16 the softmax weights are rounded to the element type before their
+ * product with V (off by at most 2^-11 and 2^-8 of each, like out's own
+ * rounding).  T == 0 or n_seqs == 0 is a no-op.
+ */
+#define QMV_PAGED_ATTENTION_WORKSPACE_BYTES (40u << 20)
+int qmv_paged_attention(const void* q, const qmv_paged_kv* kv, void* out, float* lse, int T, int n_q_heads,
+                        float scale, int causal, int window, float softcap, const float* slopes,
+                        long long q_token_stride, long long q_head_stride, long long out_token_stride,
+                        long long out_head_stride, int max_q_len, void* workspace, void* stream);
+
+/*
  * qmv_dequant_affine_f32 -- check kernel: w_out[n*K + k] = fp32 value of
  * scale * q + bias, computed with one rounding (fmaf) from the stored dtype
  * scale / bias.  Uses the same device decoders as qmv_affine.  w_out is a

@@ -24,6 +24,8 @@ __all__ = [
     "qmv_describe_plan", "qmv_force_config", "DTYPES", "FP_MODES", "LIB_PATH", "lib",
     "qmv_block_scaled", "qmv_block_scaled_batched", "qmv_dequant_block_scaled_f32", "qmv_format_info",
     "FORMATS", "qmv_test_skip_last_copy",
+    "qmv_rope", "qmv_rope_frequencies", "qmv_kv_append", "qmv_paged_attention", "ROPE_LAYOUTS", "ROPE_SCALINGS",
+    "PAGED_ATTENTION_WORKSPACE_BYTES",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -37,6 +39,9 @@ FORMATS = {name: i for i, name in enumerate(
     ["nvfp4", "mxfp4", "mxfp8_e4m3", "mxfp8_e5m2", "nvfp8", "fp4", "fp8_e4m3", "fp8_e5m2"]
     + [f"int{b}" for b in (2, 3, 4, 5, 6, 8)] + [f"mxint{b}" for b in (2, 3, 4, 5, 6, 8)]
     + ["nvfp8_f16", "fp4_f16", "fp8_e4m3_f16", "fp8_e5m2_f16"] + [f"int{b}_f16" for b in (2, 3, 4, 5, 6, 8)])}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "banded": 3}
+PAGED_ATTENTION_WORKSPACE_BYTES = 40 << 20      # QMV_PAGED_ATTENTION_WORKSPACE_BYTES of include/qmv.h
 STATUS = {0: "QMV_OK", -1: "QMV_EINVAL", -2: "QMV_EUNSUPPORTED", -3: "QMV_EALIGN", -4: "QMV_ECUDA"}
 
 if not os.path.exists(LIB_PATH):
@@ -319,6 +324,81 @@ def qmv_affine_rms_norm(x, gamma, eps, w_packed, scales, biases, y, M, N, K, bit
     _check(_lib.qmv_affine_rms_norm(_ptr(x), _ptr(gamma), ctypes.c_float(eps), _ptr(w_packed), _ptr(scales),
                                     _ptr(biases), _ptr(y), M, N, K, bits, group_size, _dtype(dtype), _stream(stream)),
            "qmv_affine_rms_norm")
+
+
+_lib.qmv_rope_frequencies.argtypes = [ctypes.POINTER(ctypes.c_float)] * 2 + [_i, ctypes.c_double, _i, ctypes.c_double,
+                                                                            _i, ctypes.c_double, ctypes.c_double]
+_lib.qmv_rope_frequencies.restype = _i
+
+
+def qmv_rope_frequencies(rot_dim, base=10000.0, scaling="plain", factor=1.0, original_length=0, turns_fast=32.0,
+                         turns_slow=1.0):
+    """Frequencies of a rotary embedding (C ABI qmv_rope_frequencies):
+    (list of rot_dim / 2 floats, magnitude), computed on the host.  scaling is
+    a name in ROPE_SCALINGS: plain, linear, base or banded."""
+    sc = scaling if isinstance(scaling, int) else ROPE_SCALINGS[scaling]
+    buf, mag = (ctypes.c_float * max(1, rot_dim // 2))(), ctypes.c_float(0.0)
+    _check(_lib.qmv_rope_frequencies(buf, ctypes.byref(mag), rot_dim, base, sc, factor, original_length, turns_fast,
+                                     turns_slow), "qmv_rope_frequencies")
+    return list(buf), mag.value
+
+
+def _layout(v):
+    return v if isinstance(v, int) else ROPE_LAYOUTS[v]
+
+
+def qmv_rope(x, y, positions, inv_freq, T, H, D, rot_dim, layout, dtype, magnitude=1.0, x_strides=None,
+             y_strides=None, stream=None):
+    """Rotary positions (C ABI qmv_rope): y [T, H, D] = x with the first
+    rot_dim dims of every head turned by positions[t] * inv_freq; layout "half"
+    or "interleaved"; strides are (token, head) in elements, dense if None;
+    y may be x."""
+    xs = x_strides or (H * D, D)
+    ys = y_strides or (H * D, D)
+    st = _fast.rope(_ptr(x), _ptr(y), _ptr(positions), _ptr(inv_freq), T, H, D, rot_dim, _layout(layout),
+                    _dtype(dtype), xs[0], xs[1], ys[0], ys[1], magnitude, _stream(stream))
+    if st:
+        raise QmvError(st, "qmv_rope")
+
+
+def qmv_kv_append(qkv, k_cache, v_cache, page_table, q_starts, kv_lens, inv_freq, q_out, T, n_q_heads, n_kv_heads,
+                  head_dim, rot_dim, layout, n_seqs, n_pages, page_size, max_pages, dtype, magnitude=1.0,
+                  positions=None, qkv_stride=None, q_out_stride=None, cache_strides=None, stream=None):
+    """Rotate and store (C ABI qmv_kv_append): the [Q | K | V] rows of
+    qmv_affine_qkv -> rotated queries in q_out, rotated keys and values in the
+    paged cache.  cache_strides is (page, token, head) in elements, None for
+    [n_pages, page_size, n_kv_heads, head_dim]; inv_freq None stores without a
+    rotation, q_out None leaves the queries alone."""
+    cs = cache_strides or (page_size * n_kv_heads * head_dim, n_kv_heads * head_dim, head_dim)
+    st = _fast.kv_append(_ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(q_starts), _ptr(kv_lens), n_pages,
+                         page_size, n_kv_heads, head_dim, _dtype(dtype), n_seqs, max_pages, cs[0], cs[1], cs[2],
+                         _ptr(qkv), _ptr(positions), _ptr(inv_freq), _ptr(q_out), T, n_q_heads, rot_dim,
+                         _layout(layout), (n_q_heads + 2 * n_kv_heads) * head_dim if qkv_stride is None else qkv_stride,
+                         n_q_heads * head_dim if q_out_stride is None else q_out_stride, magnitude, _stream(stream))
+    if st:
+        raise QmvError(st, "qmv_kv_append")
+
+
+def qmv_paged_attention(q, k_cache, v_cache, page_table, q_starts, kv_lens, out, lse, T, n_q_heads, n_kv_heads,
+                        head_dim, n_seqs, n_pages, page_size, max_pages, scale, dtype, causal=True, window=0,
+                        softcap=0.0, slopes=None, max_q_len=0, cache_strides=None, q_strides=None, out_strides=None,
+                        workspace=None, stream=None):
+    """Attention of new tokens over the paged cache (C ABI
+    qmv_paged_attention): out [T, n_q_heads, head_dim] and, unless None, lse
+    [T, n_q_heads] float32.  cache_strides as in qmv_kv_append; q_strides and
+    out_strides are (token, head) in elements.  workspace: None, or a
+    zero-filled device buffer of PAGED_ATTENTION_WORKSPACE_BYTES bytes that
+    every call leaves ready for the next."""
+    cs = cache_strides or (page_size * n_kv_heads * head_dim, n_kv_heads * head_dim, head_dim)
+    qs = q_strides or (n_q_heads * head_dim, head_dim)
+    os_ = out_strides or (n_q_heads * head_dim, head_dim)
+    st = _fast.paged_attention(_ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(q_starts), _ptr(kv_lens), n_pages,
+                               page_size, n_kv_heads, head_dim, _dtype(dtype), n_seqs, max_pages, cs[0], cs[1], cs[2],
+                               _ptr(q), _ptr(out), _ptr(lse), _ptr(slopes), _ptr(workspace), T, n_q_heads,
+                               int(bool(causal)), window, max_q_len, qs[0], qs[1], os_[0], os_[1], scale, softcap,
+                               _stream(stream))
+    if st:
+        raise QmvError(st, "qmv_paged_attention")
 
 
 def qmv_describe_plan(family, M, N, K, bits=4, group_size=64, dtype="bf16", w_align16=True) -> str:

@@ -789,6 +789,17 @@ int finish(cudaError_t e) {
     return QMV_ECUDA;
 }
 
+}  // namespace
+
+// For the C entries in other files (qmv_paged_api.cu).
+namespace qmv {
+int api_finish(cudaError_t e) { return finish(e); }
+int api_sms() { return device_sms(); }
+unsigned* api_fault_word() { return fault_word(); }
+}  // namespace qmv
+
+namespace {
+
 bool pdl_enabled() {
     static int v = -1;
     if (v < 0) {

@@ -1,0 +1,128 @@
+// qmv_paged.cuh -- what the paged-cache entry points share: the launch
+// parameters, the batch description read on the device (sequence of a token,
+// visible keys of a row, page of a position) and the host-side launch helpers.
+#pragma once
+
+#include <atomic>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace qmv {
+
+// Implemented in qmv_api.cu for the C entries that live in other files.
+int api_finish(cudaError_t e);      // QMV_OK, or QMV_ECUDA (recorded for qmv_last_cuda_error)
+int api_sms();                      // multiprocessors of the current device
+unsigned* api_fault_word();         // fault word of the current device, null if unknown
+
+// Rotation and append: rows of heads, `n_rot` rotated ones first.
+struct RopeParams {
+    const void* src;                // row t, head h at src + t * src_ts + h * src_hs
+    long long src_ts, src_hs;
+    void* dst;                      // heads [0, n_dst) go to dst + t * dst_ts + h * dst_hs
+    long long dst_ts, dst_hs;
+    int skip;                       // append: leading heads that are left alone (no q_out)
+    int n_dst;                      // heads written to dst (q); the next n_kv are K, then n_kv V
+    int n_kv;
+    int H;                          // heads of a row: n_dst + 2 n_kv
+    int T, D, rot, interleaved;
+    const int* positions;           // [T], or null: the token's place in its sequence
+    const float* inv_freq;          // [rot / 2], or null: no rotation
+    float magnitude;
+    int copy_tail;                  // 1: write dims >= rot of dst too (0: in place, they are there)
+    // paged cache (append)
+    void* k;
+    void* v;
+    long long page_s, tok_s, head_s;
+    const int* table;
+    const int* q_starts;
+    const int* kv_lens;
+    int n_seqs, n_pages, page, max_pages;
+};
+
+struct AttnParams {
+    const void* q;
+    const void* k;
+    const void* v;
+    void* out;
+    float* lse;                     // [T, Hq] or null
+    const int* table;               // [n_seqs, max_pages]
+    const int* q_starts;            // [n_seqs + 1]
+    const int* kv_lens;             // [n_seqs]
+    const float* slopes;            // [Hq] or null
+    long long q_ts, q_hs, o_ts, o_hs;
+    long long page_s, tok_s, head_s;
+    int T, Hq, Hkv, G, D;
+    int n_seqs, n_pages, page, max_pages;
+    int causal, window;             // window 0: none
+    float scale, softcap;           // softcap 0: none
+    unsigned* counters;             // workspace, null: no split over the keys
+    float* partials;
+    unsigned* fault;
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// ------------------------------------------------------------ device side --
+// q_starts[b], kept inside the T rows that exist whatever the table holds.
+__device__ __forceinline__ int row_start(const int* q_starts, int b, int T) {
+    return min(max(__ldg(q_starts + b), 0), T);
+}
+
+// Sequence that holds row t (the last b with q_starts[b] <= t), or -1 when t
+// lies before the first or behind the last sequence.
+__device__ __forceinline__ int seq_of_row(const int* q_starts, int n_seqs, int t) {
+    if (t < __ldg(q_starts) || t >= __ldg(q_starts + n_seqs)) return -1;
+    int lo = 0, hi = n_seqs;        // q_starts[lo] <= t < q_starts[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(q_starts + mid) <= t) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+// Keys [lo, hi) that the token at position pos of a sequence of len keys sees.
+__device__ __forceinline__ void visible_keys(const AttnParams& p, int pos, int len, int& lo, int& hi) {
+    hi = p.causal ? min(len, pos + 1) : len;
+    lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+    if (hi < 0) hi = 0;
+}
+
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// -------------------------------------------------------------- host side --
+// Launch with programmatic dependent launch: the kernel may begin while the
+// kernel before it drains, and waits for it before it touches memory.
+template <class Kern, class P>
+inline cudaError_t launch_dependent(Kern kern, std::atomic<unsigned>& configured, int smem_max, dim3 grid, dim3 block,
+                                    size_t smem, cudaStream_t st, const P& p) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned bit = 1u << (dev & 31);
+    if (smem_max > 48 * 1024 && !(configured.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max);
+        if (e != cudaSuccess) return e;
+        configured.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+cudaError_t launch_rope(int dtype, const RopeParams& p, int vec_bytes, cudaStream_t st);
+cudaError_t launch_attn_rows(int dtype, const AttnParams& p, cudaStream_t st);
+
+}  // namespace qmv

@@ -32,6 +32,18 @@ static int as_int(PyObject* o, int* out) {
     return 0;
 }
 
+static int as_ll(PyObject* o, long long* out) {
+    *out = PyLong_AsLongLong(o);
+    return (*out == -1 && PyErr_Occurred()) ? -1 : 0;
+}
+
+static int as_float(PyObject* o, float* out) {
+    double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) return -1;
+    *out = (float)v;
+    return 0;
+}
+
 /* affine(x, w, scales, biases, y, M, N, K, bits, group, dtype, batch, x_batched, stream) -> status */
 static PyObject* py_affine(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     (void)self;
@@ -84,10 +96,101 @@ static PyObject* py_block_scaled(PyObject* self, PyObject* const* a, Py_ssize_t 
     return PyLong_FromLong(r);
 }
 
+/* rope(x, y, positions, inv_freq, T, H, D, rot, layout, dtype, xt, xh, yt, yh, magnitude, stream) -> status */
+static PyObject* py_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    if (n != 16) { PyErr_SetString(PyExc_TypeError, "rope() takes 16 arguments"); return NULL; }
+    void* p[4];
+    int v[6];
+    long long s[4];
+    float mag;
+    void* st;
+    for (int i = 0; i < 4; ++i) if (as_ptr(a[i], &p[i])) return NULL;
+    for (int i = 0; i < 6; ++i) if (as_int(a[4 + i], &v[i])) return NULL;
+    for (int i = 0; i < 4; ++i) if (as_ll(a[10 + i], &s[i])) return NULL;
+    if (as_float(a[14], &mag) || as_ptr(a[15], &st)) return NULL;
+    int r;
+    Py_BEGIN_ALLOW_THREADS
+    r = qmv_rope(p[0], p[1], (const int*)p[2], (const float*)p[3], v[0], v[1], v[2], v[3], v[4], mag, s[0], s[1], s[2],
+                 s[3], v[5], st);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(r);
+}
+
+/* The 15 leading arguments of the two calls on a paged cache: k, v,
+ * page_table, q_starts, kv_lens, n_pages, page_size, n_kv_heads, head_dim,
+ * dtype, n_seqs, max_pages, page_stride, token_stride, head_stride. */
+static int as_cache(PyObject* const* a, qmv_paged_kv* kv) {
+    void* p[5];
+    int v[7];
+    long long s[3];
+    for (int i = 0; i < 5; ++i) if (as_ptr(a[i], &p[i])) return -1;
+    for (int i = 0; i < 7; ++i) if (as_int(a[5 + i], &v[i])) return -1;
+    for (int i = 0; i < 3; ++i) if (as_ll(a[12 + i], &s[i])) return -1;
+    kv->k = p[0]; kv->v = p[1];
+    kv->page_table = (const int*)p[2]; kv->q_starts = (const int*)p[3]; kv->kv_lens = (const int*)p[4];
+    kv->n_pages = v[0]; kv->page_size = v[1]; kv->n_kv_heads = v[2]; kv->head_dim = v[3]; kv->dtype = v[4];
+    kv->n_seqs = v[5]; kv->max_pages = v[6];
+    kv->page_stride = s[0]; kv->token_stride = s[1]; kv->head_stride = s[2];
+    return 0;
+}
+
+/* kv_append(<cache>, qkv, positions, inv_freq, q_out, T, n_q_heads, rot, layout, qkv_stride, q_out_stride,
+ * magnitude, stream) -> status */
+static PyObject* py_kv_append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    if (n != 27) { PyErr_SetString(PyExc_TypeError, "kv_append() takes 27 arguments"); return NULL; }
+    qmv_paged_kv kv;
+    void* p[4];
+    int v[4];
+    long long s[2];
+    float mag;
+    void* st;
+    if (as_cache(a, &kv)) return NULL;
+    for (int i = 0; i < 4; ++i) if (as_ptr(a[15 + i], &p[i])) return NULL;
+    for (int i = 0; i < 4; ++i) if (as_int(a[19 + i], &v[i])) return NULL;
+    for (int i = 0; i < 2; ++i) if (as_ll(a[23 + i], &s[i])) return NULL;
+    if (as_float(a[25], &mag) || as_ptr(a[26], &st)) return NULL;
+    int r;
+    Py_BEGIN_ALLOW_THREADS
+    r = qmv_kv_append(p[0], s[0], &kv, (const int*)p[1], (const float*)p[2], p[3], s[1], v[0], v[1], v[2], v[3], mag,
+                      st);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(r);
+}
+
+/* paged_attention(<cache>, q, out, lse, slopes, workspace, T, n_q_heads, causal, window, max_q_len, q_ts, q_hs,
+ * out_ts, out_hs, scale, softcap, stream) -> status */
+static PyObject* py_paged_attention(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    if (n != 32) { PyErr_SetString(PyExc_TypeError, "paged_attention() takes 32 arguments"); return NULL; }
+    qmv_paged_kv kv;
+    void* p[5];
+    int v[5];
+    long long s[4];
+    float f[2];
+    void* st;
+    if (as_cache(a, &kv)) return NULL;
+    for (int i = 0; i < 5; ++i) if (as_ptr(a[15 + i], &p[i])) return NULL;
+    for (int i = 0; i < 5; ++i) if (as_int(a[20 + i], &v[i])) return NULL;
+    for (int i = 0; i < 4; ++i) if (as_ll(a[25 + i], &s[i])) return NULL;
+    for (int i = 0; i < 2; ++i) if (as_float(a[29 + i], &f[i])) return NULL;
+    if (as_ptr(a[31], &st)) return NULL;
+    int r;
+    Py_BEGIN_ALLOW_THREADS
+    r = qmv_paged_attention(p[0], &kv, p[1], (float*)p[2], v[0], v[1], f[0], v[2], v[3], f[1], (const float*)p[3],
+                            s[0], s[1], s[2], s[3], v[4], p[4], st);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(r);
+}
+
 static PyMethodDef methods[] = {
     {"affine", (PyCFunction)(void (*)(void))py_affine, METH_FASTCALL, "qmv_affine_batched"},
     {"fp", (PyCFunction)(void (*)(void))py_fp, METH_FASTCALL, "qmv_fp_batched"},
     {"block_scaled", (PyCFunction)(void (*)(void))py_block_scaled, METH_FASTCALL, "qmv_block_scaled_batched"},
+    {"rope", (PyCFunction)(void (*)(void))py_rope, METH_FASTCALL, "qmv_rope"},
+    {"kv_append", (PyCFunction)(void (*)(void))py_kv_append, METH_FASTCALL, "qmv_kv_append"},
+    {"paged_attention", (PyCFunction)(void (*)(void))py_paged_attention, METH_FASTCALL, "qmv_paged_attention"},
     {NULL, NULL, 0, NULL},
 };
 

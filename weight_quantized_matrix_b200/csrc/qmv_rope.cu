@@ -1,0 +1,265 @@
+// qmv_rope.cu -- the rotary rotation of query / key heads, and the append of
+// rotated keys and of values to a paged cache (one kernel for both).
+//
+// Mathematics.  Pair i of a head of a token at position p turns by the angle
+// a = p * inv_freq[i]:  (x, y) -> m (x cos a - y sin a), m (x sin a + y cos a).
+// p has up to 31 bits and inv_freq 24, so an fp32 product loses the angle of a
+// far position; the product and its reduction to a fraction of one turn are
+// done in fp64 and only that fraction, in [-1/2, 1/2], is rounded to fp32 for
+// sincospif (angle error below 2^-24 turns).  The rotation itself is fp32, rounded
+// once to the element type.
+//
+// Memory-bound: every element is read once and written once.  A block takes
+// `tpb` tokens (as many as give its 256 threads two vectors each); its threads
+// first load their vectors, then share out the tokens' cosines and sines
+// through shared memory (one evaluation per token and pair, for all heads),
+// then rotate and store.  A work item is the pair of vectors a rotation mixes:
+// dims (i, i + rot/2) of the half layout, or 2 consecutive vectors of the
+// interleaved one and of the parts that are copied (dims >= rot, V).
+#include "qmv_paged.cuh"
+
+namespace qmv {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTokens = 32;      // tokens of a block
+
+template <int BYTES> struct VecOf;
+template <> struct VecOf<16> { using type = uint4; };
+template <> struct VecOf<8> { using type = uint2; };
+template <> struct VecOf<4> { using type = uint32_t; };
+template <> struct VecOf<2> { using type = uint16_t; };
+
+template <class T> __device__ __forceinline__ float to_f(T v);
+template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f<__half>(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <class T> __device__ __forceinline__ T from_f(float v);
+template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+template <class T, int E> union Vec {
+    typename VecOf<(int)sizeof(T) * E>::type raw;
+    T e[E];
+    __device__ Vec() {}
+};
+
+// One work item: where its two vectors come from and go to, and how they turn.
+struct Item {
+    const void* src[2];
+    void* dst[2];
+    int cs;                         // index of the first cos / sin, -1: copied
+    int n;                          // vectors (a head's last pair may hold one)
+    int n_turn;                     // interleaved: how many of them turn
+};
+
+struct Smem {
+    int seq_page[kMaxTokens];       // page id of the token, -1: not stored
+    int row[kMaxTokens];            // row inside the page
+    int pos[kMaxTokens];            // position that turns the heads
+    int live[kMaxTokens];           // 0: row outside every sequence
+};
+
+template <class T, int E>
+__device__ __forceinline__ bool find_item(const RopeParams& p, const Smem& s, long long t0, int ntok, int i,
+                                          int ipr_rot, int ipr_copy, Item& it) {
+    // first the heads that turn (the leading p.skip are left alone), then V
+    const int heads = p.H - p.n_kv - p.skip;
+    const int per_tok = heads * ipr_rot + p.n_kv * ipr_copy;
+    if (i >= ntok * per_tok) return false;
+    const int lt = i / per_tok;
+    int r = i - lt * per_tok;
+    int h, j;
+    const bool turns = r < heads * ipr_rot;
+    if (turns) {
+        h = r / ipr_rot;
+        j = r - h * ipr_rot;
+        h += p.skip;
+    } else {
+        r -= heads * ipr_rot;
+        h = r / ipr_copy;
+        j = r - h * ipr_copy;
+        h += p.H - p.n_kv;
+    }
+    if (!s.live[lt]) return false;
+    T* d;
+    if (h < p.n_dst) {
+        d = static_cast<T*>(p.dst) + (t0 + lt) * p.dst_ts + h * p.dst_hs;
+    } else {
+        const int pg = s.seq_page[lt];
+        if (pg < 0) return false;
+        const bool isv = h >= p.n_dst + p.n_kv;
+        const long long at = (long long)pg * p.page_s + (long long)s.row[lt] * p.tok_s +
+                             (long long)(h - p.n_dst - (isv ? p.n_kv : 0)) * p.head_s;
+        d = static_cast<T*>(isv ? p.v : p.k) + at;
+    }
+    const T* x = static_cast<const T*>(p.src) + (t0 + lt) * p.src_ts + h * p.src_hs;
+    int a, b;
+    it.cs = -1;
+    it.n = it.n_turn = 2;
+    const int rot = p.inv_freq ? p.rot : 0;
+    if (turns && !p.interleaved && j * E < rot / 2) {
+        a = j * E;
+        b = a + rot / 2;
+        it.cs = lt * (rot / 2) + a;
+    } else {
+        // two consecutive vectors
+        a = turns && !p.interleaved ? rot + (j - rot / 2 / E) * 2 * E : j * 2 * E;
+        b = a + E;
+        if (turns && p.interleaved && a < rot) it.cs = lt * (rot / 2) + a / 2;
+        if (b >= rot) it.n_turn = 1;
+        if (b >= p.D) { it.n = 1; b = a; }
+    }
+    it.src[0] = x + a; it.src[1] = x + b;
+    it.dst[0] = d + a; it.dst[1] = d + b;
+    return true;
+}
+
+template <class T, int E>
+__device__ __forceinline__ void turn(const RopeParams& p, const float2* cs, const Item& it, Vec<T, E>& a, Vec<T, E>& b) {
+    if (!p.interleaved || E == 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float2 c = cs[it.cs + e];
+            const float x = to_f(a.e[e]), y = to_f(b.e[e]);
+            a.e[e] = from_f<T>(fmaf(x, c.x, -(y * c.y)));
+            b.e[e] = from_f<T>(fmaf(x, c.y, y * c.x));
+        }
+    } else {
+        // pair k of a vector: elements 2k, 2k + 1
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            Vec<T, E>& w = v ? b : a;
+            if (v >= it.n_turn) break;
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                const float2 c = cs[it.cs + v * (E / 2) + e / 2];
+                const float x = to_f(w.e[e]), y = to_f(w.e[e + 1]);
+                w.e[e] = from_f<T>(fmaf(x, c.x, -(y * c.y)));
+                w.e[e + 1] = from_f<T>(fmaf(x, c.y, y * c.x));
+            }
+        }
+    }
+}
+
+template <class T, int E>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p, int tpb, int ipr_rot,
+                                                        int ipr_copy) {
+    using V = typename VecOf<(int)sizeof(T) * E>::type;
+    extern __shared__ __align__(16) float2 cs[];        // [tpb][rot / 2]
+    __shared__ Smem s;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const long long t0 = (long long)blockIdx.x * tpb;
+    const int ntok = (int)min((long long)tpb, p.T - t0);
+    if ((int)threadIdx.x < ntok) {
+        const int i = threadIdx.x, t = (int)t0 + i;
+        int live = 1, pos = 0, page = -1, row = 0;
+        if (p.n_kv > 0) {
+            const int b = seq_of_row(p.q_starts, p.n_seqs, t);
+            live = b >= 0;
+            if (live) {
+                const int place = __ldg(p.kv_lens + b) - __ldg(p.q_starts + b + 1) + t;
+                pos = place;
+                if (place >= 0 && place / p.page < p.max_pages) {
+                    page = __ldg(p.table + (long long)b * p.max_pages + place / p.page);
+                    row = place % p.page;
+                    if (page >= p.n_pages) page = -1;
+                }
+            }
+        }
+        if (p.positions) pos = __ldg(p.positions + t);
+        s.live[i] = live; s.pos[i] = pos; s.seq_page[i] = page; s.row[i] = row;
+    }
+    __syncthreads();
+    Item it;
+    Vec<T, E> a, b;
+    int i = threadIdx.x;
+    bool have = find_item<T, E>(p, s, t0, ntok, i, ipr_rot, ipr_copy, it);
+    if (have) {
+        a.raw = *static_cast<const V*>(it.src[0]);
+        b.raw = *static_cast<const V*>(it.src[1]);
+    }
+    const int half = p.inv_freq ? p.rot / 2 : 0;
+    for (int k = threadIdx.x; k < ntok * half; k += kThreads) {
+        const int lt = k / half;
+        const double turns = (double)s.pos[lt] * (double)__ldg(p.inv_freq + (k - lt * half)) * 0.15915494309189535;
+        float sn, c;
+        sincospif(2.0f * (float)(turns - rint(turns)), &sn, &c);
+        cs[k] = make_float2(c * p.magnitude, sn * p.magnitude);
+    }
+    __syncthreads();
+    const int per_tok = (p.H - p.n_kv - p.skip) * ipr_rot + p.n_kv * ipr_copy;
+    for (;;) {
+        if (have) {
+            const bool rot = it.cs >= 0;
+            if (rot) turn<T, E>(p, cs, it, a, b);
+            if (rot || p.copy_tail) {
+                *static_cast<V*>(it.dst[0]) = a.raw;
+                if (it.n == 2) *static_cast<V*>(it.dst[1]) = b.raw;
+            }
+        }
+        i += kThreads;
+        if (i >= ntok * per_tok) break;
+        have = find_item<T, E>(p, s, t0, ntok, i, ipr_rot, ipr_copy, it);
+        if (have) {
+            a.raw = *static_cast<const V*>(it.src[0]);
+            b.raw = *static_cast<const V*>(it.src[1]);
+        }
+    }
+}
+
+template <class T, int E> cudaError_t launch_te(const RopeParams& p, cudaStream_t st) {
+    const int rot = p.inv_freq ? p.rot : 0;
+    // items per head: pairs of the half layout plus pairs of copied vectors
+    const int ipr_rot = p.interleaved ? (p.D + 2 * E - 1) / (2 * E) : rot / 2 / E + (p.D - rot + 2 * E - 1) / (2 * E);
+    const int ipr_copy = (p.D + 2 * E - 1) / (2 * E);
+    const long long per_tok = (long long)(p.H - p.n_kv - p.skip) * ipr_rot + (long long)p.n_kv * ipr_copy;
+    if (per_tok == 0) return cudaSuccess;
+    if (per_tok > 0x3FFFFFF) return cudaErrorInvalidValue;
+    // tokens of a block: one item a thread; fewer when that would leave
+    // multiprocessors idle
+    long long tpb = kThreads / per_tok;
+    tpb = tpb < 1 ? 1 : tpb > kMaxTokens ? kMaxTokens : tpb;
+    const long long fill = ((long long)p.T + api_sms() - 1) / api_sms();
+    if (tpb > fill) tpb = fill;
+    const long long grid = (p.T + tpb - 1) / tpb;
+    if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    const size_t smem = (size_t)tpb * (rot / 2) * sizeof(float2);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;       // at most 32 tokens x 128 pairs x 8 bytes = 32 KB
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, rope_kernel<T, E>, p, (int)tpb, ipr_rot, ipr_copy);
+}
+
+template <class T> cudaError_t launch_t(const RopeParams& p, int vec_bytes, cudaStream_t st) {
+    constexpr int ES = (int)sizeof(T);
+    if (vec_bytes >= 16) return launch_te<T, 16 / ES>(p, st);
+    if (vec_bytes == 8) return launch_te<T, 8 / ES>(p, st);
+    if constexpr (ES == 2) {
+        if (vec_bytes == 4) return launch_te<T, 2>(p, st);
+    }
+    return launch_te<T, 1>(p, st);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(int dtype, const RopeParams& p, int vec_bytes, cudaStream_t st) {
+    switch (dtype) {
+        case 0: return launch_t<float>(p, vec_bytes, st);
+        case 1: return launch_t<__half>(p, vec_bytes, st);
+        case 2: return launch_t<__nv_bfloat16>(p, vec_bytes, st);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace qmv
