@@ -1,0 +1,440 @@
+// qmv_attn_few.cu -- attention over a paged cache for few query rows a kv head
+// (one-token decode, drafted tokens): 16-bit types.
+//
+// Bound by the keys and values, which are read once per kv head: a unit's 16 packed
+// rows (the G query heads of 16 / G tokens) share them.
+//  * Each of the 4 warps streams its own 16 of a tile's 64 keys through its own
+//    ring in shared memory (cp.async, 16-byte chunks, XOR-swizzled so that
+//    ldmatrix is free of conflicts); a warp waits only for its own copies, and
+//    no block-wide barrier lies inside the key loop.  2 blocks an SM keep about
+//    190 KB in flight (D = 128), four times what the latency needs.
+//  * S = Q K^T and O += P V run on mma.sync m16n8k16 (fp32 accumulators in
+//    registers): 16 rows is the whole problem, so the 128-row tcgen05 tiles would be
+//    7/8 empty, and at 16 rows the products take a fifth of the copy's time.
+//  * The running maximum, the weights' sum and the output are per warp, and meet
+//    once per unit in shared memory.  The output is rescaled only when a maximum
+//    grows.  The weights are rounded to the element type for the second
+//    product (their sum is not): the error is that of rounding the output.
+//  * The heads' dims are padded to DP = 64, 128 or 256 with zeros in shared
+//    memory only.
+#include <limits.h>
+
+#include <algorithm>
+
+#include "qmv_attn_sched.cuh"
+
+namespace qmv {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kRows = 16;
+constexpr int kTile = 64;            // keys of a tile, 16 a warp
+
+template <int DP> struct FewGeom {
+    static constexpr int STAGES = DP == 64 ? 6 : 3;
+    static constexpr int PER_SM = DP == 256 ? 1 : 2;
+    static constexpr int ROWB = DP * 2;                    // bytes of a key in shared memory
+    static constexpr int STEP = 2 * 16 * ROWB;             // a warp's K and V of one tile
+    static constexpr int RING = kWarps * STAGES * STEP;
+};
+static_assert(kWarps * kRows * 256 * 4 <= FewGeom<256>::RING && kWarps * kRows * 64 * 4 <= FewGeom<64>::RING, "joined in the ring");
+
+__device__ __forceinline__ uint32_t s_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool read) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+template <class T> __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <> __device__ __forceinline__ void mma<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <> __device__ __forceinline__ void mma<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <class T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <class T> __device__ __forceinline__ float2 unpack2(uint32_t v);
+template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t v) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+template <> __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t v) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+// Whether either half of a word is infinite or NaN.
+template <class T> __device__ __forceinline__ bool odd_word(uint32_t v) {
+    constexpr uint32_t E = sizeof(T) == 2 && __is_same(T, __half) ? 0x7C00u : 0x7F80u;
+    return (v & E) == E || ((v >> 16) & E) == E;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <class T, int DP, bool MOD>
+__global__ void __launch_bounds__(kWarps * 32, FewGeom<DP>::PER_SM) attn_few_kernel(const __grid_constant__ AttnParams p,
+                                                                                 int page_shift) {
+    using Gm = FewGeom<DP>;
+    constexpr int STAGES = Gm::STAGES, ROWB = Gm::ROWB, KS = DP / 16, NT = DP / 8, CPR = DP / 8;
+    extern __shared__ __align__(1024) unsigned char ring[];
+    __shared__ SchedSmem sm;
+    __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+    __shared__ int s_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int gid = lane >> 2, tig = lane & 3;
+    unsigned char* mine = ring + warp * STAGES * Gm::STEP;
+    const uint32_t mine_a = s_addr(mine);
+    const int chunks = p.D / 8;                     // 16-byte chunks of a head
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    Sched<kRows, kTile> sc;
+    sc.init<kWarps * 32, 1>(p, sm, 2);
+    const ScoreMod mod(p);
+    const float scale2 = p.scale * kLog2e;
+    const T* kc = static_cast<const T*>(p.k);
+    const T* vc = static_cast<const T*>(p.v);
+
+    while (sc.live) {
+        int k0, k1;
+        sc.piece(k0, k1);
+        const SeqInfo s = sc.s;
+        const int rbase = sc.i * kRows, nrows = min(kRows, s.n * p.G - rbase);
+        int ulo, uhi;                               // keys that any row of the unit sees
+        rows_keys(p, s, rbase, rbase + nrows - 1, ulo, uhi);
+        const T* kh = kc + (long long)sc.h * p.head_s;
+        const T* vh = vc + (long long)sc.h * p.head_s;
+        const int* trow = p.table + (long long)sc.b * p.max_pages;
+
+        // lane r < 16: place of key r of this warp's next step, fetched one
+        // step ahead of its use; -1 outside the unit's keys, -2 on a bad page
+        auto place = [&](int t) -> long long {
+            const int j = t * kTile + warp * 16 + (lane & 15);
+            if (t >= k1 || j < ulo || j >= uhi) return -1;
+            const int e = page_shift >= 0 ? j >> page_shift : j / p.page;
+            if (e >= p.max_pages) return -2;
+            const int pg = __ldg(trow + e);
+            if ((unsigned)pg >= (unsigned)p.n_pages) return -2;
+            return (long long)pg * p.page_s + (long long)(j - e * p.page) * p.tok_s;
+        };
+        auto issue = [&](int t, int slot, long long at) {
+            if (t < k1) {
+                const uint32_t base = mine_a + slot * Gm::STEP;
+                const bool odd = __any_sync(0xFFFFFFFFu, at == -2);
+#pragma unroll
+                for (int u = 0; u < 16 * CPR / 32; ++u) {
+                    const int id = u * 32 + lane, r = id / CPR, c = id % CPR;
+                    const long long a = __shfl_sync(0xFFFFFFFFu, at, r);
+                    const uint32_t d = base + r * ROWB + ((c ^ (r & 7)) << 4);
+                    const bool rd = a >= 0 && c < chunks;
+                    const long long off = rd ? a + c * 8 : 0;
+                    cp16(d, kh + off, rd);
+                    cp16(d + 16 * ROWB, vh + off, rd);
+                }
+                if (odd) {                          // keys of NaN, once the copies have landed
+                    cp_commit();
+                    cp_wait<0>();
+                    __syncwarp();
+                    for (int u = 0; u < 16 * CPR / 32; ++u) {
+                        const int id = u * 32 + lane, r = id / CPR, c = id % CPR;
+                        if (__shfl_sync(0xFFFFFFFFu, at, r) == -2 && c == 0)
+                            *reinterpret_cast<uint4*>(mine + slot * Gm::STEP + r * ROWB + ((c ^ (r & 7)) << 4)) =
+                                make_uint4(~0u, ~0u, ~0u, ~0u);
+                    }
+                    return;
+                }
+            }
+            cp_commit();
+        };
+
+        // ---- queries: A fragments, rows gid and gid + 8 ---------------------
+        uint32_t qf[KS][4];
+        int lo[2], hi[2], pos[2];
+        float slope[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = gid + 8 * e;
+            const bool in = r < nrows;
+            const int pr = rbase + (in ? r : 0), ti = pr / p.G, h = sc.h * p.G + pr - ti * p.G;
+            pos[e] = s.len - s.n + ti;
+            visible_keys(p, pos[e], s.len, lo[e], hi[e]);
+            if (!in) lo[e] = hi[e] = 0;
+            slope[e] = MOD && p.slopes ? __ldg(p.slopes + h) * kLog2e : 0.0f;
+            const T* qr = static_cast<const T*>(p.q) + (long long)(s.t0 + ti) * p.q_ts + (long long)h * p.q_hs;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int d = k * 16 + u * 8 + tig * 2;
+                    qf[k][e + 2 * u] = in && d < p.D ? *reinterpret_cast<const uint32_t*>(qr + d) : 0u;
+                }
+            }
+        }
+        // keys that every row sees: no masks there
+        int alo = max(lo[0], nrows > gid + 8 ? lo[1] : 0), ahi = min(gid < nrows ? hi[0] : INT_MAX, gid + 8 < nrows ? hi[1] : INT_MAX);
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) {
+            alo = max(alo, __shfl_xor_sync(0xFFFFFFFFu, alo, w));
+            ahi = min(ahi, __shfl_xor_sync(0xFFFFFFFFu, ahi, w));
+        }
+        float o[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+
+        long long at = place(k0);
+#pragma unroll
+        for (int t = 0; t < STAGES - 1; ++t) {
+            const long long nx = place(k0 + t + 1);
+            issue(k0 + t, t, at);
+            at = nx;
+        }
+        int slot = 0;
+        for (int t = k0; t < k1; ++t) {
+            const long long nx = place(t + STAGES);
+            cp_wait<STAGES - 2>();
+            __syncwarp();
+            {
+                const int fs = slot == 0 ? STAGES - 1 : slot - 1;     // the stage read last time
+                issue(t + STAGES - 1, fs, at);
+                at = nx;
+            }
+            const uint32_t kb = mine_a + slot * Gm::STEP, vb = kb + 16 * ROWB;
+            slot = slot + 1 == STAGES ? 0 : slot + 1;
+            const int j0 = t * kTile + warp * 16;
+            if (j0 >= uhi || j0 + 16 <= ulo) continue;
+
+            // ---- S = Q K^T: 16 rows x 16 keys ---------------------------------
+            float sa[2][4] = {}, sb[2][4] = {};     // two chains of half the dims
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                uint32_t f[4];                      // keys 0-7 / 8-15 x dims 0-7 / 8-15
+                const int r = (lane & 7) + ((lane >> 4) << 3), c = 2 * k + ((lane >> 3) & 1);
+                ldsm4(kb + r * ROWB + ((c ^ (r & 7)) << 4), f);
+                if (k & 1) {
+                    mma<T>(sb[0], qf[k], f[0], f[1]);
+                    mma<T>(sb[1], qf[k], f[2], f[3]);
+                } else {
+                    mma<T>(sa[0], qf[k], f[0], f[1]);
+                    mma<T>(sa[1], qf[k], f[2], f[3]);
+                }
+            }
+            // element (n, 2e + u): row gid + 8 e, key j0 + 8 n + 2 tig + u
+            const bool full = j0 >= alo && j0 + 16 <= ahi;
+            float mx[2] = {m[0], m[1]};
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int e = x >> 1, j = j0 + 8 * n + 2 * tig + (x & 1);
+                    float v = sa[n][x] + sb[n][x];
+                    if constexpr (MOD) v = mod.apply(v, slope[e], j - pos[e]);
+                    else v *= scale2;
+                    if (!full && (j < lo[e] || j >= hi[e])) v = -INFINITY;
+                    sa[n][x] = v;
+                    mx[e] = fmaxf(mx[e], v);
+                }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 1));
+                mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 2));
+            }
+            if (__any_sync(0xFFFFFFFFu, mx[0] > m[0] || mx[1] > m[1])) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float f = m[e] == -INFINITY ? 0.0f : ex2(m[e] - mx[e]);
+                    l[e] *= f;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) { o[n][2 * e] *= f; o[n][2 * e + 1] *= f; }
+                    m[e] = mx[e];
+                }
+            }
+            const float base[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    sa[n][x] = ex2(sa[n][x] - base[x >> 1]);
+                    l[x >> 1] += sa[n][x];
+                }
+            // ---- O += P V -----------------------------------------------------
+            // Where some rows see a key and others do not, an infinite or NaN
+            // value must not reach the others through 0 * v: such a step (no
+            // finite model makes one) adds key by key.
+            bool odd = false;
+            if (!full) {
+                for (int u = 0; u < 16 * CPR / 32; ++u) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(mine + (vb - mine_a) + (u * 32 + lane) * 16);
+                    odd |= odd_word<T>(w.x) || odd_word<T>(w.y) || odd_word<T>(w.z) || odd_word<T>(w.w);
+                }
+                odd = __any_sync(0xFFFFFFFFu, odd);
+            }
+            if (!odd) {
+                uint32_t pf[4] = {pack2<T>(sa[0][0], sa[0][1]), pack2<T>(sa[0][2], sa[0][3]),
+                                  pack2<T>(sa[1][0], sa[1][1]), pack2<T>(sa[1][2], sa[1][3])};
+#pragma unroll
+                for (int n = 0; n < NT; n += 2) {
+                    uint32_t f[4];                  // keys 0-7 / 8-15 of dims 8n.., then of the next 8
+                    const int r = lane & 15, c = n + (lane >> 4);
+                    ldsm4t(vb + r * ROWB + ((c ^ (r & 7)) << 4), f);
+                    mma<T>(o[n], pf, f[0], f[1]);
+                    mma<T>(o[n + 1], pf, f[2], f[3]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const int j = j0 + k, src = (lane & ~3) | ((k & 7) >> 1);
+                    const float p0 = __shfl_sync(0xFFFFFFFFu, sa[k >> 3][k & 1], src);
+                    const float p1 = __shfl_sync(0xFFFFFFFFu, sa[k >> 3][2 + (k & 1)], src);
+                    const bool v0 = j >= lo[0] && j < hi[0], v1 = j >= lo[1] && j < hi[1];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const float2 w = unpack2<T>(*reinterpret_cast<const uint32_t*>(
+                            mine + (vb - mine_a) + k * ROWB + ((n ^ (k & 7)) << 4) + tig * 4));
+                        if (v0) { o[n][0] = fmaf(p0, w.x, o[n][0]); o[n][1] = fmaf(p0, w.y, o[n][1]); }
+                        if (v1) { o[n][2] = fmaf(p1, w.x, o[n][2]); o[n][3] = fmaf(p1, w.y, o[n][3]); }
+                    }
+                }
+            }
+        }
+        cp_wait<0>();
+        __syncthreads();
+
+        // ---- the warps' results meet in the ring ------------------------------
+        float* red = reinterpret_cast<float*>(ring);            // [warp][row][DP]
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 1);
+            l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 2);
+            if (tig == 0) { s_m[warp][gid + 8 * e] = m[e]; s_l[warp][gid + 8 * e] = l[e]; }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                *reinterpret_cast<float2*>(red + (warp * kRows + gid + 8 * e) * DP + n * 8 + tig * 2) =
+                    make_float2(o[n][2 * e], o[n][2 * e + 1]);
+        }
+        __syncthreads();
+        const bool part = sc.shared();
+        float* slot_o = part ? attn_slot(p, blockIdx.x, sc.w0 >= sc.us ? 0 : 1, kRows) : nullptr;
+        float* slot_m = slot_o + kRows * p.D;
+        auto store = [&](int r, int d, float v, float mm, float ll) {
+            const int pr = rbase + r, ti = pr / p.G, h = sc.h * p.G + pr - ti * p.G;
+            const long long t = s.t0 + ti;
+            if (d < 0) {
+                if (p.lse) p.lse[t * p.Hq + h] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+            } else {
+                st_elem(static_cast<T*>(p.out) + t * p.o_ts + (long long)h * p.o_hs + d, ll == 0.0f ? 0.0f : v / ll);
+            }
+        };
+        for (int x = threadIdx.x; x < nrows * p.D; x += kWarps * 32) {
+            const int r = x / p.D, d = x - r * p.D;
+            float mm = s_m[0][r];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, s_m[w][r]);
+            float v = 0.0f, ll = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = s_m[w][r] == -INFINITY && !(s_l[w][r] != s_l[w][r]) ? 0.0f
+                              : ex2(s_m[w][r] == -INFINITY ? 0.0f : s_m[w][r] - mm);
+                v = fmaf(red[(w * kRows + r) * DP + d], f, v);
+                ll = fmaf(s_l[w][r], f, ll);
+            }
+            if (part) {
+                __stcg(slot_o + r * p.D + d, v);
+                if (d == 0) { __stcg(slot_m + r, mm); __stcg(slot_m + kRows + r, ll); }
+            } else {
+                store(r, d, v, mm, ll);
+                if (d == 0) store(r, -1, v, mm, ll);
+            }
+        }
+        if (part && attn_arrive(p, sc, &s_flag, threadIdx.x == 0, [] { __syncthreads(); })) {
+            const int c0 = sc.owner(sc.us), c1 = sc.owner(sc.us + sc.c - 1);
+            for (int x = threadIdx.x; x < nrows * p.D; x += kWarps * 32) {
+                const int r = x / p.D, d = x - r * p.D;
+                float mm = -INFINITY, v = 0.0f, ll = 0.0f;
+#pragma unroll 4
+                for (int c = c0; c <= c1; ++c) {
+                    const float* so = attn_slot(p, c, sc.part(c) >= sc.us ? 0 : 1, kRows);
+                    const float om = __ldcg(so + kRows * p.D + r), ol = __ldcg(so + kRows * p.D + kRows + r);
+                    const float ov = __ldcg(so + r * p.D + d);
+                    if (ol == 0.0f) continue;
+                    const float mn = fmaxf(mm, om), b0 = mn == -INFINITY ? 0.0f : mn;
+                    const float f0 = mm == -INFINITY && ll == 0.0f ? 0.0f : ex2(mm == -INFINITY ? 0.0f : mm - b0);
+                    const float f1 = ex2(om == -INFINITY ? 0.0f : om - b0);
+                    v = fmaf(ov, f1, v * f0);
+                    ll = fmaf(ol, f1, ll * f0);
+                    mm = mn;
+                }
+                store(r, d, v, mm, ll);
+                if (d == 0) store(r, -1, v, mm, ll);
+            }
+        }
+        __syncthreads();
+        sc.next(p);
+    }
+}
+
+template <class T, int DP, bool MOD> cudaError_t launch_tdm(const AttnParams& p, cudaStream_t st) {
+    using Gm = FewGeom<DP>;
+    static std::atomic<unsigned> configured{0};
+    auto kern = attn_few_kernel<T, DP, MOD>;
+    int shift = -1;
+    if ((p.page & (p.page - 1)) == 0)
+        for (shift = 0; (1 << shift) < p.page; ++shift) {}
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned bit = 1u << (dev & 31);
+    if (!(configured.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Gm::RING);
+        if (e != cudaSuccess) return e;
+        configured.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(std::min(api_sms(), 148) * Gm::PER_SM));
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = Gm::RING;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p, shift);
+}
+
+template <class T, int DP> cudaError_t launch_td(const AttnParams& p, cudaStream_t st) {
+    return p.softcap > 0.0f || p.slopes ? launch_tdm<T, DP, true>(p, st) : launch_tdm<T, DP, false>(p, st);
+}
+
+template <class T> cudaError_t launch_t(const AttnParams& p, cudaStream_t st) {
+    return p.D <= 64 ? launch_td<T, 64>(p, st) : p.D <= 128 ? launch_td<T, 128>(p, st) : launch_td<T, 256>(p, st);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_few(int dtype, const AttnParams& p, cudaStream_t st) {
+    return dtype == 1 ? launch_t<__half>(p, st) : launch_t<__nv_bfloat16>(p, st);
+}
+
+}  // namespace qmv

@@ -1,0 +1,223 @@
+// qmv_attn_sched.cuh -- how the attention kernels share out their work.
+//
+// A unit is (sequence b, kv head h, row tile i): ROWS consecutive packed rows of
+// a sequence (packed row r is query head h G + r % G of new token r / G, so the
+// G query heads that share a kv head share its keys), over the keys that any of
+// them sees, in key tiles of TK.  All units' key tiles, laid end to end in the
+// order (b, h, i), are cut into equal parts, one a block: every block streams
+// the same number of key tiles whatever the lengths are, and nothing but the
+// device's length lists decides the cut (a captured call can be replayed with
+// other lengths).  Each block finds its own part: it sums the units' tile
+// counts over the sequences with a block-wide scan.
+//
+// A block whose part ends or begins inside a unit leaves that unit's partial
+// result (unnormalised sums, maxima, weights) in the workspace and counts
+// itself in on the unit's counter; the last block to arrive joins the parts in
+// block order, writes the unit's output and sets the counter back to zero.  No
+// block waits for another, and the order of every sum depends on the arguments
+// alone.  Without a workspace a unit belongs whole to the block in whose part it
+// begins.
+#pragma once
+
+#include "qmv_attn.cuh"
+
+namespace qmv {
+
+constexpr int kAttnCounters = 4096;                     // unsigned words at the workspace's start
+constexpr size_t kAttnPartialsAt = kAttnCounters * 4;   // byte offset of the partial results
+
+struct SeqInfo {
+    int t0, n, len;         // first row, new tokens, keys
+};
+
+__device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int b) {
+    SeqInfo s;
+    s.t0 = row_start(p.q_starts, b, p.T);
+    s.n = max(0, row_start(p.q_starts, b + 1, p.T) - s.t0);
+    s.len = max(0, __ldg(p.kv_lens + b));
+    return s;
+}
+
+// Keys [lo, hi) that any of the packed rows r0..r1 of a sequence sees (0, 0: none).
+__device__ __forceinline__ void rows_keys(const AttnParams& p, const SeqInfo& s, int r0, int r1, int& lo, int& hi) {
+    int x;
+    visible_keys(p, s.len - s.n + r0 / p.G, s.len, lo, x);
+    visible_keys(p, s.len - s.n + r1 / p.G, s.len, x, hi);
+    if (lo >= hi) lo = hi = 0;
+}
+
+// Row tile i of a sequence: its first key tile and the number of key tiles (0:
+// the unit sees no key; it still counts as one tile of work).
+template <int ROWS, int TK>
+__device__ __forceinline__ int unit_tiles(const AttnParams& p, const SeqInfo& s, int i, int& first) {
+    int lo, hi;
+    rows_keys(p, s, i * ROWS, min((i + 1) * ROWS, s.n * p.G) - 1, lo, hi);
+    first = lo / TK;
+    return (hi + TK - 1) / TK - first;
+}
+
+struct SchedSmem {
+    long long warp_sum[32];
+    long long seq_at;       // tiles before the sequence in which the block's part begins
+    int seq;                // that sequence
+    long long per_head;     // its tiles per kv head
+};
+
+// One block's walk over its part.
+template <int ROWS, int TK> struct Sched {
+    long long W, w0, w1;    // all tiles, this block's part
+    long long us;           // first tile of the current unit
+    int nblk, b, h, i, c;   // blocks with a part; current unit and its cost in tiles
+    int first, nt;          // its first key tile and number of key tiles
+    SeqInfo s;
+    bool split, live;
+
+    __device__ __forceinline__ long long part(int blk) const { return W * blk / nblk; }
+    __device__ __forceinline__ int owner(long long w) const { return (int)(((w + 1) * nblk - 1) / W); }
+
+    __device__ __forceinline__ void load_unit(const AttnParams& p) {
+        nt = unit_tiles<ROWS, TK>(p, s, i, first);
+        c = max(nt, 1);
+    }
+    __device__ __forceinline__ void next(const AttnParams& p) {
+        us += c;
+        if (++i * ROWS >= s.n * p.G) {
+            i = 0;
+            if (++h == p.Hkv) {
+                h = 0;
+                do {
+                    if (++b >= p.n_seqs) { live = false; return; }
+                    s = seq_info(p, b);
+                } while (s.n == 0);
+            }
+        }
+        if (us >= w1) { live = false; return; }
+        load_unit(p);
+    }
+    // Every thread of the block calls this (NT threads, LPS lanes a sequence).
+    template <int NT, int LPS> __device__ __forceinline__ void init(const AttnParams& p, SchedSmem& sm, int min_tiles) {
+        constexpr int SEQS = NT / LPS;
+        const int tid = threadIdx.x, lane = tid & 31, sub = tid % LPS;
+        auto cost = [&](int bb) {
+            long long v = 0;
+            if (bb < p.n_seqs) {
+                const SeqInfo si = seq_info(p, bb);
+                const int nq = (si.n * p.G + ROWS - 1) / ROWS;
+                int f;
+                for (int k = sub; k < nq; k += LPS) v += max(unit_tiles<ROWS, TK>(p, si, k, f), 1);
+            }
+#pragma unroll
+            for (int w = LPS / 2; w > 0; w >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, w);
+            return v;
+        };
+        // inclusive scan over the block (the value counts once a sequence)
+        auto scan = [&](long long v, long long& total) {
+            v = sub == 0 ? v * p.Hkv : 0;
+#pragma unroll
+            for (int w = 1; w < 32; w <<= 1) {
+                const long long u = __shfl_up_sync(0xFFFFFFFFu, v, w);
+                if (lane >= w) v += u;
+            }
+            __syncthreads();
+            if (lane == 31) sm.warp_sum[tid >> 5] = v;
+            __syncthreads();
+            long long before = 0;
+            total = 0;
+#pragma unroll
+            for (int w = 0; w < NT / 32; ++w) {
+                const long long u = sm.warp_sum[w];
+                if (w < (tid >> 5)) before += u;
+                total += u;
+            }
+            return v + before;
+        };
+        split = p.partials != nullptr;
+        live = false;
+        W = 0;
+        const int rounds = (p.n_seqs + SEQS - 1) / SEQS;
+        long long v = 0, incl = 0;
+        for (int r = 0; r < rounds; ++r) {
+            v = cost(r * SEQS + tid / LPS);
+            long long total;
+            incl = scan(v, total);
+            W += total;
+        }
+        if (W == 0) return;
+        nblk = (int)min((long long)gridDim.x, max(1LL, W / min_tiles));
+        if ((int)blockIdx.x >= nblk) return;
+        w0 = part(blockIdx.x);
+        w1 = part(blockIdx.x + 1);
+        long long base = 0;
+        for (int r = 0; r < rounds; ++r) {
+            long long total = W;
+            if (rounds > 1) {
+                v = cost(r * SEQS + tid / LPS);
+                incl = scan(v, total);
+            }
+            const long long end = base + incl, beg = end - v * p.Hkv;
+            if (sub == 0 && beg <= w0 && w0 < end) {
+                sm.seq = r * SEQS + tid / LPS;
+                sm.seq_at = beg;
+                sm.per_head = v;
+            }
+            base += total;
+            if (base > w0) break;       // the same for every thread
+        }
+        __syncthreads();
+        b = sm.seq;
+        s = seq_info(p, b);
+        long long off = w0 - sm.seq_at;
+        h = (int)(off / sm.per_head);
+        off -= h * sm.per_head;
+        i = 0;
+        load_unit(p);
+        while (off >= c) {
+            off -= c;
+            ++i;
+            load_unit(p);
+        }
+        us = w0 - off;
+        live = true;
+        if (!split && off > 0) next(p);     // the unit belongs to the block before
+    }
+    // Key tiles [k0, k1) of the current unit that are this block's.
+    __device__ __forceinline__ void piece(int& k0, int& k1) const {
+        if (split) {
+            k0 = first + (int)(max(w0, us) - us);
+            k1 = first + min((int)(min(w1, us + c) - us), nt);
+        } else {
+            k0 = first;
+            k1 = first + nt;
+        }
+    }
+    // Whether other blocks hold parts of the current unit.
+    __device__ __forceinline__ bool shared() const { return split && (us < w0 || us + c > w1); }
+};
+
+// Partial result of a block: slot 0 for the unit its part begins in, 1 for the
+// one it ends in.  Per slot ROWS x D sums, then ROWS maxima (log2) and weights.
+__device__ __forceinline__ float* attn_slot(const AttnParams& p, int blk, int which, int rows) {
+    return p.partials + ((size_t)blk * 2 + which) * ((size_t)rows * (p.D + 2));
+}
+
+// Counts this block in on the current unit; true in the last one to arrive.
+// Every thread of the `nthreads` that call it has written its share before.
+template <int ROWS, int TK, class Sync>
+__device__ __forceinline__ bool attn_arrive(const AttnParams& p, const Sched<ROWS, TK>& sc, int* s_flag, bool first_thread,
+                                            Sync sync) {
+    const int c0 = sc.owner(sc.us), c1 = sc.owner(sc.us + sc.c - 1);
+    __threadfence();
+    sync();
+    if (first_thread) {
+        const unsigned old = atomicAdd(p.counters + c0, 1u);
+        const bool last = old == (unsigned)(c1 - c0);
+        if (last) p.counters[c0] = 0u;
+        *s_flag = last;
+    }
+    sync();
+    const bool last = *s_flag != 0;
+    if (last) __threadfence();
+    return last;
+}
+
+}  // namespace qmv

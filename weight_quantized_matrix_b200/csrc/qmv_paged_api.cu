@@ -5,7 +5,7 @@
 #include <initializer_list>
 
 #include "qmv.h"
-#include "qmv_paged.cuh"
+#include "qmv_attn_sched.cuh"
 
 namespace {
 
@@ -199,6 +199,7 @@ int qmv_paged_attention(const void* q, const qmv_paged_kv* kv, void* out, float*
     int st = check_cache(kv);
     if (st != QMV_OK) return st;
     if (T < 0 || n_q_heads < 1 || n_q_heads % kv->n_kv_heads != 0 || max_q_len < 0) return QMV_EINVAL;
+    if ((long long)T * n_q_heads > 0x7FFFFFFF) return QMV_EUNSUPPORTED;
     if (causal != 0 && causal != 1) return QMV_EINVAL;
     if (window < 0 || !(softcap >= 0.0f) || isinf(softcap) || !(scale > 0.0f) || isinf(scale)) return QMV_EINVAL;
     const int D = kv->head_dim;
@@ -222,7 +223,18 @@ int qmv_paged_attention(const void* q, const qmv_paged_kv* kv, void* out, float*
     p.causal = causal;
     p.window = window > (1 << 30) ? 0 : window;      // wider than any position: none
     p.scale = scale; p.softcap = softcap;
-    return qmv::api_finish(qmv::launch_attn_rows(kv->dtype, p, static_cast<cudaStream_t>(stream)));
+    if (workspace) {
+        p.counters = static_cast<unsigned*>(workspace);
+        p.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + qmv::kAttnPartialsAt);
+    }
+    auto s = static_cast<cudaStream_t>(stream);
+    // 16-byte copies of whole heads: the kernels that stream keys and values
+    const int vec = common_vec({(long long)reinterpret_cast<uintptr_t>(q), (long long)reinterpret_cast<uintptr_t>(kv->k),
+                                (long long)reinterpret_cast<uintptr_t>(kv->v), q_token_stride * (long long)eb,
+                                q_head_stride * (long long)eb, kv->page_stride * (long long)eb,
+                                kv->token_stride * (long long)eb, kv->head_stride * (long long)eb, D * (long long)eb});
+    if (kv->dtype != QMV_F32 && vec == 16) return qmv::api_finish(qmv::launch_attn_few(kv->dtype, p, s));
+    return qmv::api_finish(qmv::launch_attn_rows(kv->dtype, p, s));
 }
 
 }  // extern "C"
