@@ -39,6 +39,7 @@ template <int DP> struct FewGeom {
     static constexpr int RING = kWarps * STAGES * STEP;
 };
 static_assert(kWarps * kRows * 256 * 4 <= FewGeom<256>::RING && kWarps * kRows * 64 * 4 <= FewGeom<64>::RING, "joined in the ring");
+static_assert(kJoinBytes <= FewGeom<64>::RING, "joined in the ring");
 
 __device__ __forceinline__ uint32_t s_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool read) {
@@ -336,59 +337,38 @@ __global__ void __launch_bounds__(kWarps * 32, FewGeom<DP>::PER_SM) attn_few_ker
         __syncthreads();
         const bool part = sc.shared();
         float* slot_o = part ? attn_slot(p, blockIdx.x, sc.w0 >= sc.us ? 0 : 1, kRows) : nullptr;
-        float* slot_m = slot_o + kRows * p.D;
-        auto store = [&](int r, int d, float v, float mm, float ll) {
+        auto store = [&](int r, int d, float4 v, float mm, float ll) {
             const int pr = rbase + r, ti = pr / p.G, h = sc.h * p.G + pr - ti * p.G;
-            const long long t = s.t0 + ti;
-            if (d < 0) {
-                if (p.lse) p.lse[t * p.Hq + h] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
-            } else {
-                st_elem(static_cast<T*>(p.out) + t * p.o_ts + (long long)h * p.o_hs + d, ll == 0.0f ? 0.0f : v / ll);
-            }
+            const long long row = s.t0 + ti;
+            const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;    // no key: 0 even where a sum is not a number
+            if (ll == 0.0f) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            T* to = static_cast<T*>(p.out) + row * p.o_ts + (long long)h * p.o_hs + d;
+            st_elem(to, v.x * inv); st_elem(to + 1, v.y * inv); st_elem(to + 2, v.z * inv); st_elem(to + 3, v.w * inv);
+            if (d == 0 && p.lse) p.lse[row * p.Hq + h] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
         };
-        for (int x = threadIdx.x; x < nrows * p.D; x += kWarps * 32) {
-            const int r = x / p.D, d = x - r * p.D;
+        for (int x = threadIdx.x; x < nrows * (DP / 4); x += kWarps * 32) {
+            const int r = x / (DP / 4), d = (x % (DP / 4)) * 4;
+            if (d >= p.D) continue;
             float mm = s_m[0][r];
 #pragma unroll
             for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, s_m[w][r]);
-            float v = 0.0f, ll = 0.0f;
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float ll = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float f = s_m[w][r] == -INFINITY && !(s_l[w][r] != s_l[w][r]) ? 0.0f
-                              : ex2(s_m[w][r] == -INFINITY ? 0.0f : s_m[w][r] - mm);
-                v = fmaf(red[(w * kRows + r) * DP + d], f, v);
+                const float f = part_weight(s_m[w][r], s_l[w][r], mm);
+                const float4 u = *reinterpret_cast<const float4*>(red + (w * kRows + r) * DP + d);
+                v.x = fmaf(u.x, f, v.x); v.y = fmaf(u.y, f, v.y); v.z = fmaf(u.z, f, v.z); v.w = fmaf(u.w, f, v.w);
                 ll = fmaf(s_l[w][r], f, ll);
             }
             if (part) {
-                __stcg(slot_o + r * p.D + d, v);
-                if (d == 0) { __stcg(slot_m + r, mm); __stcg(slot_m + kRows + r, ll); }
+                __stcg(reinterpret_cast<float4*>(slot_o + r * p.D + d), v);
+                if (d == 0) { __stcg(slot_o + kRows * p.D + r, mm); __stcg(slot_o + kRows * p.D + kRows + r, ll); }
             } else {
                 store(r, d, v, mm, ll);
-                if (d == 0) store(r, -1, v, mm, ll);
             }
         }
-        if (part && attn_arrive(p, sc, &s_flag, threadIdx.x == 0, [] { __syncthreads(); })) {
-            const int c0 = sc.owner(sc.us), c1 = sc.owner(sc.us + sc.c - 1);
-            for (int x = threadIdx.x; x < nrows * p.D; x += kWarps * 32) {
-                const int r = x / p.D, d = x - r * p.D;
-                float mm = -INFINITY, v = 0.0f, ll = 0.0f;
-#pragma unroll 4
-                for (int c = c0; c <= c1; ++c) {
-                    const float* so = attn_slot(p, c, sc.part(c) >= sc.us ? 0 : 1, kRows);
-                    const float om = __ldcg(so + kRows * p.D + r), ol = __ldcg(so + kRows * p.D + kRows + r);
-                    const float ov = __ldcg(so + r * p.D + d);
-                    if (ol == 0.0f) continue;
-                    const float mn = fmaxf(mm, om), b0 = mn == -INFINITY ? 0.0f : mn;
-                    const float f0 = mm == -INFINITY && ll == 0.0f ? 0.0f : ex2(mm == -INFINITY ? 0.0f : mm - b0);
-                    const float f1 = ex2(om == -INFINITY ? 0.0f : om - b0);
-                    v = fmaf(ov, f1, v * f0);
-                    ll = fmaf(ol, f1, ll * f0);
-                    mm = mn;
-                }
-                store(r, d, v, mm, ll);
-                if (d == 0) store(r, -1, v, mm, ll);
-            }
-        }
+        if (part && attn_arrive(p, sc, &s_flag)) attn_join<kWarps * 32>(p, sc, nrows, ring, store);
         __syncthreads();
         sc.next(p);
     }

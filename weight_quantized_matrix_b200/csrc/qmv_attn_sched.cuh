@@ -63,17 +63,27 @@ struct SchedSmem {
     long long per_head;     // its tiles per kv head
 };
 
+// a / b; 32-bit when both fit (a 64-bit division is a call of a hundred instructions).
+__device__ __forceinline__ long long tile_div(long long a, long long b) {
+    if (((a | b) >> 31) == 0) return (long long)((unsigned)a / (unsigned)b);
+    return a / b;
+}
+
 // One block's walk over its part.
 template <int ROWS, int TK> struct Sched {
     long long W, w0, w1;    // all tiles, this block's part
+    long long q, rem;       // W = nblk q + rem: the first rem blocks take q + 1 tiles
     long long us;           // first tile of the current unit
     int nblk, b, h, i, c;   // blocks with a part; current unit and its cost in tiles
     int first, nt;          // its first key tile and number of key tiles
     SeqInfo s;
     bool split, live;
 
-    __device__ __forceinline__ long long part(int blk) const { return W * blk / nblk; }
-    __device__ __forceinline__ int owner(long long w) const { return (int)(((w + 1) * nblk - 1) / W); }
+    __device__ __forceinline__ long long part(int blk) const { return blk * q + min((long long)blk, rem); }
+    __device__ __forceinline__ int owner(long long w) const {
+        const long long big = rem * (q + 1);
+        return (int)(w < big ? tile_div(w, q + 1) : rem + tile_div(w - big, q));
+    }
 
     __device__ __forceinline__ void load_unit(const AttnParams& p) {
         nt = unit_tiles<ROWS, TK>(p, s, i, first);
@@ -143,8 +153,10 @@ template <int ROWS, int TK> struct Sched {
             W += total;
         }
         if (W == 0) return;
-        nblk = (int)min((long long)gridDim.x, max(1LL, W / min_tiles));
+        nblk = (int)min((long long)gridDim.x, max(1LL, tile_div(W, min_tiles)));
         if ((int)blockIdx.x >= nblk) return;
+        q = tile_div(W, nblk);
+        rem = W - q * nblk;
         w0 = part(blockIdx.x);
         w1 = part(blockIdx.x + 1);
         long long base = 0;
@@ -167,7 +179,7 @@ template <int ROWS, int TK> struct Sched {
         b = sm.seq;
         s = seq_info(p, b);
         long long off = w0 - sm.seq_at;
-        h = (int)(off / sm.per_head);
+        h = (int)tile_div(off, sm.per_head);
         off -= h * sm.per_head;
         i = 0;
         load_unit(p);
@@ -195,29 +207,89 @@ template <int ROWS, int TK> struct Sched {
 };
 
 // Partial result of a block: slot 0 for the unit its part begins in, 1 for the
-// one it ends in.  Per slot ROWS x D sums, then ROWS maxima (log2) and weights.
+// one it ends in.  Per slot ROWS x D sums, then ROWS maxima (log2) and sums of
+// weights.
 __device__ __forceinline__ float* attn_slot(const AttnParams& p, int blk, int which, int rows) {
     return p.partials + ((size_t)blk * 2 + which) * ((size_t)rows * (p.D + 2));
 }
 
 // Counts this block in on the current unit; true in the last one to arrive.
-// Every thread of the `nthreads` that call it has written its share before.
-template <int ROWS, int TK, class Sync>
-__device__ __forceinline__ bool attn_arrive(const AttnParams& p, const Sched<ROWS, TK>& sc, int* s_flag, bool first_thread,
-                                            Sync sync) {
-    const int c0 = sc.owner(sc.us), c1 = sc.owner(sc.us + sc.c - 1);
+// Every thread of the block has written its share before.
+template <int ROWS, int TK>
+__device__ __forceinline__ bool attn_arrive(const AttnParams& p, const Sched<ROWS, TK>& sc, int* s_flag) {
     __threadfence();
-    sync();
-    if (first_thread) {
-        const unsigned old = atomicAdd(p.counters + c0, 1u);
-        const bool last = old == (unsigned)(c1 - c0);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const int c0 = sc.owner(sc.us), c1 = sc.owner(sc.us + sc.c - 1);
+        const bool last = atomicAdd(p.counters + c0, 1u) == (unsigned)(c1 - c0);
         if (last) p.counters[c0] = 0u;
         *s_flag = last;
     }
-    sync();
+    __syncthreads();
     const bool last = *s_flag != 0;
     if (last) __threadfence();
     return last;
+}
+
+// Weight of a partial result whose maximum (log2) is m among ones of maximum M:
+// 0 for one without keys.
+__device__ __forceinline__ float part_weight(float m, float l, float M) {
+    return l == 0.0f ? 0.0f : exp2f(m == -INFINITY && M == -INFINITY ? 0.0f : m - M);
+}
+
+// The last block joins the parts of the current unit (whole block; NT threads;
+// at most kJoinParts parts and kJoinRows rows).  store(row, dim, 4 sums, m, l)
+// gets every 4 dims of every row.
+constexpr int kJoinParts = 296, kJoinRows = 16;
+constexpr int kJoinBytes = kJoinParts * 4 + 2 * kJoinRows * kJoinParts * 4 + 2 * kJoinRows * 4;
+template <int NT, int ROWS, int TK, class Store>
+__device__ __forceinline__ void attn_join(const AttnParams& p, const Sched<ROWS, TK>& sc, int nrows, void* buf, Store store) {
+    static_assert(ROWS <= kJoinRows, "join buffer");
+    const int c0 = sc.owner(sc.us), np = sc.owner(sc.us + sc.c - 1) - c0 + 1;
+    float* s_f = static_cast<float*>(buf);              // [row][np]: maximum, then weight
+    float* s_l = s_f + ROWS * np;
+    float* s_M = s_l + ROWS * np;
+    float* s_L = s_M + ROWS;
+    int* s_slot = reinterpret_cast<int*>(s_L + ROWS);
+    const int tid = threadIdx.x, lane = tid & 31;
+    for (int i = tid; i < np; i += NT) s_slot[i] = (c0 + i) * 2 + (sc.part(c0 + i) >= sc.us ? 0 : 1);
+    __syncthreads();
+    const size_t ss = (size_t)ROWS * (p.D + 2);
+    for (int x = tid; x < nrows * np; x += NT) {
+        const int r = x / np, i = x - r * np;
+        const float* so = p.partials + s_slot[i] * ss + ROWS * p.D;
+        s_f[x] = __ldcg(so + r);
+        s_l[x] = __ldcg(so + ROWS + r);
+    }
+    __syncthreads();
+    for (int r = tid >> 5; r < nrows; r += NT / 32) {
+        float M = -INFINITY, L = 0.0f;
+        for (int i = lane; i < np; i += 32) M = fmaxf(M, s_f[r * np + i]);
+#pragma unroll
+        for (int w = 16; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, w));
+        for (int i = lane; i < np; i += 32) {
+            const float l = s_l[r * np + i], f = part_weight(s_f[r * np + i], l, M);
+            s_f[r * np + i] = f;
+            L = fmaf(l, f, L);
+        }
+#pragma unroll
+        for (int w = 16; w > 0; w >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, w);
+        if (lane == 0) { s_M[r] = M; s_L[r] = L; }
+    }
+    __syncthreads();
+    const int vecs = p.D / 4;
+    for (int x = tid; x < nrows * vecs; x += NT) {
+        const int r = x / vecs, d = (x - r * vecs) * 4;
+        const float* so = p.partials + r * p.D + d;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+        for (int i = 0; i < np; ++i) {
+            const float4 u = __ldcg(reinterpret_cast<const float4*>(so + s_slot[i] * ss));
+            const float f = s_f[r * np + i];
+            v.x = fmaf(u.x, f, v.x); v.y = fmaf(u.y, f, v.y); v.z = fmaf(u.z, f, v.z); v.w = fmaf(u.w, f, v.w);
+        }
+        store(r, d, v, s_M[r], s_L[r]);
+    }
 }
 
 }  // namespace qmv
