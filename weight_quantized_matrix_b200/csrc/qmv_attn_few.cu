@@ -42,7 +42,10 @@ static_assert(kWarps * kRows * 256 * 4 <= FewGeom<256>::RING && kWarps * kRows *
 static_assert(kJoinBytes <= FewGeom<64>::RING, "joined in the ring");
 
 __device__ __forceinline__ uint32_t s_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool read) {
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void* src, bool read) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -111,11 +114,10 @@ __global__ void __launch_bounds__(kWarps * 32, FewGeom<DP>::PER_SM) attn_few_ker
     grid_launch_dependents();
 
     Sched<kRows, kTile> sc;
-    sc.init<kWarps * 32, 1>(p, sm, 2);
+    sc.init<kWarps * 32, 1>(p, sm, 12);
     const ScoreMod mod(p);
     const float scale2 = p.scale * kLog2e;
-    const T* kc = static_cast<const T*>(p.k);
-    const T* vc = static_cast<const T*>(p.v);
+    const int page16 = (int)(p.page_s / 8), tok16 = (int)(p.tok_s / 8);
 
     while (sc.live) {
         int k0, k1;
@@ -124,46 +126,54 @@ __global__ void __launch_bounds__(kWarps * 32, FewGeom<DP>::PER_SM) attn_few_ker
         const int rbase = sc.i * kRows, nrows = min(kRows, s.n * p.G - rbase);
         int ulo, uhi;                               // keys that any row of the unit sees
         rows_keys(p, s, rbase, rbase + nrows - 1, ulo, uhi);
-        const T* kh = kc + (long long)sc.h * p.head_s;
-        const T* vh = vc + (long long)sc.h * p.head_s;
+        // this lane's chunk of the head's rows
+        const char* kl = static_cast<const char*>(p.k) + (long long)sc.h * p.head_s * 2 + lane % CPR * 16;
+        const char* vl = static_cast<const char*>(p.v) + (long long)sc.h * p.head_s * 2 + lane % CPR * 16;
         const int* trow = p.table + (long long)sc.b * p.max_pages;
 
-        // lane r < 16: place of key r of this warp's next step, fetched one
-        // step ahead of its use; -1 outside the unit's keys, -2 on a bad page
-        auto place = [&](int t) -> long long {
+        // lanes r and r + 16: place of key r of this warp's step t, in units of 16
+        // bytes; -1 outside the unit's keys, -2 on a bad page
+        auto place = [&](int t) -> int {
             const int j = t * kTile + warp * 16 + (lane & 15);
             if (t >= k1 || j < ulo || j >= uhi) return -1;
             const int e = page_shift >= 0 ? j >> page_shift : j / p.page;
             if (e >= p.max_pages) return -2;
             const int pg = __ldg(trow + e);
             if ((unsigned)pg >= (unsigned)p.n_pages) return -2;
-            return (long long)pg * p.page_s + (long long)(j - e * p.page) * p.tok_s;
+            return pg * page16 + (j - e * p.page) * tok16;
         };
-        auto issue = [&](int t, int slot, long long at) {
+        auto issue = [&](int t, int slot, int at) {
             if (t < k1) {
                 const uint32_t base = mine_a + slot * Gm::STEP;
-                const bool odd = __any_sync(0xFFFFFFFFu, at == -2);
+                if (chunks == CPR && __all_sync(0xFFFFFFFFu, at >= 0)) {
 #pragma unroll
-                for (int u = 0; u < 16 * CPR / 32; ++u) {
-                    const int id = u * 32 + lane, r = id / CPR, c = id % CPR;
-                    const long long a = __shfl_sync(0xFFFFFFFFu, at, r);
-                    const uint32_t d = base + r * ROWB + ((c ^ (r & 7)) << 4);
-                    const bool rd = a >= 0 && c < chunks;
-                    const long long off = rd ? a + c * 8 : 0;
-                    cp16(d, kh + off, rd);
-                    cp16(d + 16 * ROWB, vh + off, rd);
-                }
-                if (odd) {                          // keys of NaN, once the copies have landed
-                    cp_commit();
-                    cp_wait<0>();
-                    __syncwarp();
                     for (int u = 0; u < 16 * CPR / 32; ++u) {
                         const int id = u * 32 + lane, r = id / CPR, c = id % CPR;
-                        if (__shfl_sync(0xFFFFFFFFu, at, r) == -2 && c == 0)
-                            *reinterpret_cast<uint4*>(mine + slot * Gm::STEP + r * ROWB + ((c ^ (r & 7)) << 4)) =
-                                make_uint4(~0u, ~0u, ~0u, ~0u);
+                        const long long off = (long long)__shfl_sync(0xFFFFFFFFu, at, r) * 16;
+                        const uint32_t d = base + r * ROWB + ((c ^ (r & 7)) << 4);
+                        cp16(d, kl + off);
+                        cp16(d + 16 * ROWB, vl + off);
                     }
-                    return;
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 16 * CPR / 32; ++u) {
+                        const int id = u * 32 + lane, r = id / CPR, c = id % CPR;
+                        const int a = __shfl_sync(0xFFFFFFFFu, at, r);
+                        const uint32_t d = base + r * ROWB + ((c ^ (r & 7)) << 4);
+                        const bool rd = a >= 0 && c < chunks;
+                        const long long off = rd ? (long long)a * 16 : -16 * c;
+                        cp16_or_zero(d, kl + off, rd);
+                        cp16_or_zero(d + 16 * ROWB, vl + off, rd);
+                    }
+                    if (__any_sync(0xFFFFFFFFu, at == -2)) {        // keys of NaN, once the copies have landed
+                        cp_commit();
+                        cp_wait<0>();
+                        __syncwarp();
+                        if (lane < 16 && at == -2)
+                            *reinterpret_cast<uint4*>(mine + slot * Gm::STEP + lane * ROWB + ((lane & 7) << 4)) =
+                                make_uint4(~0u, ~0u, ~0u, ~0u);
+                        return;
+                    }
                 }
             }
             cp_commit();
@@ -204,23 +214,26 @@ __global__ void __launch_bounds__(kWarps * 32, FewGeom<DP>::PER_SM) attn_few_ker
         for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 
-        long long at = place(k0);
+        // places of the next AHEAD steps to issue: the table's latency is behind
+        // as many steps
+        constexpr int AHEAD = 4;
+        int at[AHEAD];
 #pragma unroll
-        for (int t = 0; t < STAGES - 1; ++t) {
-            const long long nx = place(k0 + t + 1);
-            issue(k0 + t, t, at);
-            at = nx;
-        }
+        for (int u = 0; u < AHEAD; ++u) at[u] = place(k0 + u);
+        auto issue_next = [&](int t, int slot) {
+            const int now = at[0];
+#pragma unroll
+            for (int u = 0; u + 1 < AHEAD; ++u) at[u] = at[u + 1];
+            at[AHEAD - 1] = place(t + AHEAD);
+            issue(t, slot, now);
+        };
+#pragma unroll
+        for (int t = 0; t < STAGES - 1; ++t) issue_next(k0 + t, t);
         int slot = 0;
         for (int t = k0; t < k1; ++t) {
-            const long long nx = place(t + STAGES);
             cp_wait<STAGES - 2>();
             __syncwarp();
-            {
-                const int fs = slot == 0 ? STAGES - 1 : slot - 1;     // the stage read last time
-                issue(t + STAGES - 1, fs, at);
-                at = nx;
-            }
+            issue_next(t + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1);     // the stage read last time
             const uint32_t kb = mine_a + slot * Gm::STEP, vb = kb + 16 * ROWB;
             slot = slot + 1 == STAGES ? 0 : slot + 1;
             const int j0 = t * kTile + warp * 16;
@@ -249,13 +262,22 @@ __global__ void __launch_bounds__(kWarps * 32, FewGeom<DP>::PER_SM) attn_few_ker
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const int e = x >> 1, j = j0 + 8 * n + 2 * tig + (x & 1);
-                    float v = sa[n][x] + sb[n][x];
-                    if constexpr (MOD) v = mod.apply(v, slope[e], j - pos[e]);
-                    else v *= scale2;
-                    if (!full && (j < lo[e] || j >= hi[e])) v = -INFINITY;
-                    sa[n][x] = v;
-                    mx[e] = fmaxf(mx[e], v);
+                    sa[n][x] += sb[n][x];
+                    if constexpr (MOD) sa[n][x] = mod.apply(sa[n][x], slope[e], j - pos[e]);
+                    else sa[n][x] *= scale2;
                 }
+            if (!full) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int e = x >> 1, j = j0 + 8 * n + 2 * tig + (x & 1);
+                        if (j < lo[e] || j >= hi[e]) sa[n][x] = -INFINITY;
+                    }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                mx[e] = fmaxf(fmaxf(fmaxf(sa[0][2 * e], sa[0][2 * e + 1]), fmaxf(sa[1][2 * e], sa[1][2 * e + 1])), mx[e]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 1));

@@ -10,6 +10,10 @@
 // other lengths).  Each block finds its own part: it sums the units' tile
 // counts over the sequences with a block-wide scan.
 //
+// Few tiles a block are cut at the units' own ends instead (every unit into
+// parts of Q tiles, the last one shorter), as long as that gives no more parts
+// than blocks: a block that ends one unit and begins another pays two joins.
+//
 // A block whose part ends or begins inside a unit leaves that unit's partial
 // result (unnormalised sums, maxima, weights) in the workspace and counts
 // itself in on the unit's counter; the last block to arrive joins the parts in
@@ -56,6 +60,8 @@ __device__ __forceinline__ int unit_tiles(const AttnParams& p, const SeqInfo& s,
     return (hi + TK - 1) / TK - first;
 }
 
+constexpr int kAlignTiles = 64;         // parts up to this many tiles end with their units
+
 struct SchedSmem {
     long long warp_sum[32];
     long long seq_at;       // tiles before the sequence in which the block's part begins
@@ -76,9 +82,13 @@ template <int ROWS, int TK> struct Sched {
     long long us;           // first tile of the current unit
     int nblk, b, h, i, c;   // blocks with a part; current unit and its cost in tiles
     int first, nt;          // its first key tile and number of key tiles
+    int Q;                  // costs are rounded up to multiples of Q
     SeqInfo s;
     bool split, live;
 
+    __device__ __forceinline__ int padded(int tiles) const {
+        return tiles <= Q ? Q : Q == 1 ? tiles : (tiles + Q - 1) / Q * Q;
+    }
     __device__ __forceinline__ long long part(int blk) const { return blk * q + min((long long)blk, rem); }
     __device__ __forceinline__ int owner(long long w) const {
         const long long big = rem * (q + 1);
@@ -87,7 +97,7 @@ template <int ROWS, int TK> struct Sched {
 
     __device__ __forceinline__ void load_unit(const AttnParams& p) {
         nt = unit_tiles<ROWS, TK>(p, s, i, first);
-        c = max(nt, 1);
+        c = padded(nt);
     }
     __device__ __forceinline__ void next(const AttnParams& p) {
         us += c;
@@ -108,13 +118,20 @@ template <int ROWS, int TK> struct Sched {
     template <int NT, int LPS> __device__ __forceinline__ void init(const AttnParams& p, SchedSmem& sm, int min_tiles) {
         constexpr int SEQS = NT / LPS;
         const int tid = threadIdx.x, lane = tid & 31, sub = tid % LPS;
+        int only = -1;          // tiles of the thread's sequence where it has one row tile and there is one round
+        const int rounds = (p.n_seqs + SEQS - 1) / SEQS;
         auto cost = [&](int bb) {
             long long v = 0;
+            if (LPS == 1 && only >= 0) return (long long)padded(only);
             if (bb < p.n_seqs) {
                 const SeqInfo si = seq_info(p, bb);
                 const int nq = (si.n * p.G + ROWS - 1) / ROWS;
                 int f;
-                for (int k = sub; k < nq; k += LPS) v += max(unit_tiles<ROWS, TK>(p, si, k, f), 1);
+                for (int k = sub; k < nq; k += LPS) {
+                    const int tiles = unit_tiles<ROWS, TK>(p, si, k, f);
+                    if (nq == 1 && rounds == 1) only = tiles;
+                    v += padded(tiles);
+                }
             }
 #pragma unroll
             for (int w = LPS / 2; w > 0; w >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, w);
@@ -143,17 +160,32 @@ template <int ROWS, int TK> struct Sched {
         };
         split = p.partials != nullptr;
         live = false;
-        W = 0;
-        const int rounds = (p.n_seqs + SEQS - 1) / SEQS;
         long long v = 0, incl = 0;
-        for (int r = 0; r < rounds; ++r) {
-            v = cost(r * SEQS + tid / LPS);
-            long long total;
-            incl = scan(v, total);
-            W += total;
-        }
+        auto count = [&]() {
+            W = 0;
+            for (int r = 0; r < rounds; ++r) {
+                v = cost(r * SEQS + tid / LPS);
+                long long total;
+                incl = scan(v, total);
+                W += total;
+            }
+        };
+        Q = 1;
+        count();
         if (W == 0) return;
         nblk = (int)min((long long)gridDim.x, max(1LL, tile_div(W, min_tiles)));
+        const long long each = tile_div(W + gridDim.x - 1, gridDim.x);
+        if (split && each <= kAlignTiles) {
+            const long long all = W;
+            Q = max((int)each, min_tiles);
+            count();
+            if (tile_div(W, Q) <= gridDim.x) {
+                nblk = (int)tile_div(W, Q);
+            } else {
+                Q = 1;
+                if (rounds > 1) W = all; else count();
+            }
+        }
         if ((int)blockIdx.x >= nblk) return;
         q = tile_div(W, nblk);
         rem = W - q * nblk;

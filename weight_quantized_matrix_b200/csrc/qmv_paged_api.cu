@@ -233,7 +233,9 @@ int qmv_paged_attention(const void* q, const qmv_paged_kv* kv, void* out, float*
                                 (long long)reinterpret_cast<uintptr_t>(kv->v), q_token_stride * (long long)eb,
                                 q_head_stride * (long long)eb, kv->page_stride * (long long)eb,
                                 kv->token_stride * (long long)eb, kv->head_stride * (long long)eb, D * (long long)eb});
-    if (kv->dtype != QMV_F32 && vec == 16) return qmv::api_finish(qmv::launch_attn_few(kv->dtype, p, s));
+    // whose places (in 16 bytes) fit an int: caches of up to 32 GiB a tensor
+    const bool near = (kv->n_pages - 1LL) * kv->page_stride + (kv->page_size - 1LL) * kv->token_stride <= (8LL << 31) - 8;
+    if (kv->dtype != QMV_F32 && vec == 16 && near) return qmv::api_finish(qmv::launch_attn_few(kv->dtype, p, s));
     return qmv::api_finish(qmv::launch_attn_rows(kv->dtype, p, s));
 }
 
