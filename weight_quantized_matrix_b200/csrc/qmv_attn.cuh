@@ -23,20 +23,29 @@ __device__ __forceinline__ long long key_place(const AttnParams& p, int b, int h
 }
 
 // Dot product -> score in units of log2: scale, then the cap c tanh(s / c),
-// then the distance bias.  tanh(x) = 1 - 2 / (2^(2x log2 e) + 1): exact limits at
-// both ends, absolute error of a few 2^-24 (the hardware's tanh approximation
-// has 2^-11, which the cap would multiply into the score).
-struct ScoreMod {
+// then the distance bias.  EXACT (fp32 elements) takes tanhf.  For 16-bit
+// elements tanh(x) = 1 - 2 / (2^(2x log2 e) + 1), with exact limits at both ends and
+// an absolute error below 2^-20 (the hardware's tanh approximation has 2^-11,
+// which the cap would multiply into the score).
+template <bool EXACT> struct ScoreMod {
     float pre, post;
     bool cap;
     __device__ explicit ScoreMod(const AttnParams& p) {
         cap = p.softcap > 0.0f;
-        pre = cap ? p.scale / p.softcap * (2.0f * kLog2e) : p.scale * kLog2e;
+        pre = !cap ? p.scale * kLog2e : EXACT ? p.scale / p.softcap : p.scale / p.softcap * (2.0f * kLog2e);
         post = p.softcap * kLog2e;
     }
     __device__ __forceinline__ float apply(float dot, float slope_log2, int away) const {
         float s = dot * pre;
-        if (cap) s = post - post * 2.0f / (exp2f(s) + 1.0f);
+        if (cap) {
+            if constexpr (EXACT) {
+                s = post * tanhf(s);
+            } else {
+                float e;
+                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(s));
+                s = fmaf(-post, __fdividef(2.0f, e + 1.0f), post);
+            }
+        }
         return fmaf(slope_log2, (float)away, s);
     }
 };

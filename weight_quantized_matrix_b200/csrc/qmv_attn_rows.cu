@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) attn_rows_kernel(const __grid_
     grid_launch_dependents();
     const int lane = threadIdx.x & 31;
     const long long rows = (long long)p.T * p.Hq;
-    const ScoreMod mod(p);
+    const ScoreMod<true> mod(p);
     for (long long r = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5); r < rows;
          r += (long long)gridDim.x * kRowWarps) {
         const int t = (int)(r / p.Hq), h = (int)(r - (long long)t * p.Hq);

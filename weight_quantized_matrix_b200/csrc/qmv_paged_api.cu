@@ -235,7 +235,13 @@ int qmv_paged_attention(const void* q, const qmv_paged_kv* kv, void* out, float*
                                 kv->token_stride * (long long)eb, kv->head_stride * (long long)eb, D * (long long)eb});
     // whose places (in 16 bytes) fit an int: caches of up to 32 GiB a tensor
     const bool near = (kv->n_pages - 1LL) * kv->page_stride + (kv->page_size - 1LL) * kv->token_stride <= (8LL << 31) - 8;
-    if (kv->dtype != QMV_F32 && vec == 16 && near) return qmv::api_finish(qmv::launch_attn_few(kv->dtype, p, s));
+    if (kv->dtype != QMV_F32 && vec == 16 && near) {
+        p.fault = qmv::api_fault_word();
+        if (!p.fault) return QMV_ECUDA;
+        const long long rows = (long long)(max_q_len > 0 && max_q_len < T ? max_q_len : T) * p.G;
+        if (rows > 16 && D <= 128) return qmv::api_finish(qmv::launch_attn_chunk(kv->dtype, p, s));
+        return qmv::api_finish(qmv::launch_attn_few(kv->dtype, p, s));
+    }
     return qmv::api_finish(qmv::launch_attn_rows(kv->dtype, p, s));
 }
 
