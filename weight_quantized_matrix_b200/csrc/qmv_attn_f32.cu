@@ -1,0 +1,356 @@
+// qmv_attn_f32.cu -- attention over a paged cache for fp32 elements.
+//
+// The products are fp32 FMAs (the tensor cores have no fp32 form; splitting the
+// operands would lose to the copies at the few rows this type is decoded with).
+// One-token and drafted decode is bound by the keys and values, which a unit's 16
+// packed rows share; long chunks are bound by the FMAs and the shared-memory
+// reads that feed them.
+//  * As in qmv_attn_few.cu every warp streams its own 16 keys of a tile through its
+//    own ring (cp.async, 16-byte chunks, XOR-swizzled).
+//  * Scores: lane = (key, half of the dims); a 16-byte read of the key serves up to
+//    16 rows, whose queries are broadcast reads.  Rows go in fours, and fours
+//    that the unit does not have are skipped.
+//  * Weights go through shared memory; for the second product a lane owns D / 32
+//    dims of every row, V is read once for all rows.
+//  * DP = 64, 128 or 256 dims, padded with zeros in shared memory only.
+#include <limits.h>
+
+#include <algorithm>
+
+#include "qmv_attn_mma.cuh"
+#include "qmv_attn_sched.cuh"
+
+namespace qmv {
+
+namespace {
+
+constexpr int kRows = 16;
+
+template <int DP> struct F32Geom {
+    static constexpr int WARPS = DP == 256 ? 2 : 4;
+    static constexpr int TILE = 16 * WARPS;
+    static constexpr int STAGES = 3;
+    static constexpr int PER_SM = DP == 64 ? 2 : 1;
+    static constexpr int ROWB = DP * 4;
+    static constexpr int STEP = 2 * 16 * ROWB;
+    static constexpr int RING = WARPS * STAGES * STEP;
+    static constexpr int QH = DP / 2 + 4;                    // floats of half a query row; the halves fall on other banks
+    static constexpr int SMEM = RING + kRows * 2 * QH * 4;
+};
+static_assert(kJoinBytes <= F32Geom<64>::RING, "joined in the ring");
+
+// 32 lanes x VEC dims: lane's dims are 4-float groups lane, lane + 32 (D = 256), or a pair (D = 64)
+template <int DP, bool MOD>
+__global__ void __launch_bounds__(F32Geom<DP>::WARPS * 32, F32Geom<DP>::PER_SM)
+attn_f32_kernel(const __grid_constant__ AttnParams p, int page_shift) {
+    using Gm = F32Geom<DP>;
+    constexpr int WARPS = Gm::WARPS, NTH = WARPS * 32, STAGES = Gm::STAGES, ROWB = Gm::ROWB, CPR = DP / 4, VEC = DP / 32;
+    extern __shared__ __align__(1024) unsigned char ring[];
+    float* s_q = reinterpret_cast<float*>(ring + Gm::RING);
+    __shared__ SchedSmem sm;
+    __shared__ __align__(16) float s_p[WARPS][kRows][16];
+    __shared__ float s_m[WARPS][kRows], s_l[WARPS][kRows];
+    __shared__ int s_lo[kRows], s_hi[kRows], s_pos[kRows];
+    __shared__ float s_slope[kRows];
+    __shared__ int s_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    unsigned char* mine = ring + warp * STAGES * Gm::STEP;
+    const uint32_t mine_a = s_addr(mine);
+    const int chunks = p.D / 4;
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    Sched<kRows, Gm::TILE> sc;
+    sc.template init<NTH, 1>(p, sm, 12);
+    const ScoreMod<true> mod(p);
+    const int page16 = (int)(p.page_s / 4), tok16 = (int)(p.tok_s / 4);
+
+    while (sc.live) {
+        int k0, k1;
+        sc.piece(k0, k1);
+        const SeqInfo s = sc.s;
+        const int rbase = sc.i * kRows, nrows = min(kRows, s.n * p.G - rbase);
+        int ulo, uhi;
+        rows_keys(p, s, rbase, rbase + nrows - 1, ulo, uhi);
+        const char* kh = static_cast<const char*>(p.k) + (long long)sc.h * p.head_s * 4;
+        const char* vh = static_cast<const char*>(p.v) + (long long)sc.h * p.head_s * 4;
+        const int* trow = p.table + (long long)sc.b * p.max_pages;
+        auto place = [&](int t) -> int {
+            const int j = t * Gm::TILE + warp * 16 + (lane & 15);
+            if (t >= k1 || j < ulo || j >= uhi) return -1;
+            const int e = page_shift >= 0 ? j >> page_shift : j / p.page;
+            if (e >= p.max_pages) return -2;
+            const int pg = __ldg(trow + e);
+            if ((unsigned)pg >= (unsigned)p.n_pages) return -2;
+            return pg * page16 + (j - e * p.page) * tok16;
+        };
+        auto issue = [&](int t, int slot, int at) {
+            if (t < k1) {
+                const uint32_t base = mine_a + slot * Gm::STEP;
+#pragma unroll 8
+                for (int u = 0; u < 16 * CPR / 32; ++u) {
+                    const int id = u * 32 + lane, r = id / CPR, c = id % CPR;
+                    const int a = __shfl_sync(0xFFFFFFFFu, at, r);
+                    const uint32_t d = base + r * ROWB + ((c ^ (r & 7)) << 4);
+                    const bool rd = a >= 0 && c < chunks;
+                    const long long off = rd ? (long long)a * 16 + c * 16 : 0;
+                    cp16_or_zero(d, kh + off, rd);
+                    cp16_or_zero(d + 16 * ROWB, vh + off, rd);
+                }
+                if (__any_sync(0xFFFFFFFFu, at == -2)) {            // keys of NaN, once the copies have landed
+                    cp_commit();
+                    cp_wait<0>();
+                    __syncwarp();
+                    if (lane < 16 && at == -2)
+                        *reinterpret_cast<uint4*>(mine + slot * Gm::STEP + lane * ROWB + ((lane & 7) << 4)) =
+                            make_uint4(~0u, ~0u, ~0u, ~0u);
+                    return;
+                }
+            }
+            cp_commit();
+        };
+        constexpr int AHEAD = 4;
+        int at[AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) at[u] = place(k0 + u);
+        auto issue_next = [&](int t, int slot) {
+            const int now = at[0];
+#pragma unroll
+            for (int u = 0; u + 1 < AHEAD; ++u) at[u] = at[u + 1];
+            at[AHEAD - 1] = place(t + AHEAD);
+            issue(t, slot, now);
+        };
+#pragma unroll
+        for (int t = 0; t < STAGES - 1; ++t) issue_next(k0 + t, t);
+
+        // ---- queries and the rows' keys --------------------------------------
+        for (int x = threadIdx.x; x < kRows * CPR; x += NTH) {
+            const int r = x / CPR, c = x % CPR, pr = rbase + min(r, nrows - 1), ti = pr / p.G;
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (r < nrows && c < chunks)
+                v = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + (long long)(s.t0 + ti) * p.q_ts +
+                                                     (long long)(sc.h * p.G + pr - ti * p.G) * p.q_hs + c * 4);
+            *reinterpret_cast<float4*>(s_q + (r * 2 + c / (CPR / 2)) * Gm::QH + c % (CPR / 2) * 4) = v;
+        }
+        if (threadIdx.x < kRows) {
+            const int r = threadIdx.x, pr = rbase + min(r, nrows - 1), ti = pr / p.G, h = sc.h * p.G + pr - ti * p.G;
+            int lo, hi;
+            s_pos[r] = s.len - s.n + ti;
+            visible_keys(p, s_pos[r], s.len, lo, hi);
+            s_lo[r] = r < nrows ? lo : 0;
+            s_hi[r] = r < nrows ? hi : 0;
+            s_slope[r] = p.slopes ? __ldg(p.slopes + h) * kLog2e : 0.0f;
+        }
+        __syncthreads();
+        // keys that every row sees (bounds ascend with the row)
+        const int alo = s_lo[nrows - 1], ahi = s_hi[0];
+
+        float o[kRows][VEC], m[kRows], l[kRows];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.0f;
+#pragma unroll
+            for (int u = 0; u < VEC; ++u) o[r][u] = 0.0f;
+        }
+        int slot = 0;
+        for (int t = k0; t < k1; ++t) {
+            cp_wait<STAGES - 2>();
+            __syncwarp();
+            issue_next(t + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1);
+            const unsigned char* kb = mine + slot * Gm::STEP;
+            const unsigned char* vb = kb + 16 * ROWB;
+            slot = slot + 1 == STAGES ? 0 : slot + 1;
+            const int j0 = t * Gm::TILE + warp * 16;
+            if (j0 >= uhi || j0 + 16 <= ulo) continue;
+            const bool full = j0 >= alo && j0 + 16 <= ahi;
+
+            // ---- scores: lane = (key, half of the dims) -------------------------
+            const int key = lane & 15, hf = lane >> 4, j = j0 + key;
+            float x[kRows];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) x[r] = 0.0f;
+#pragma unroll 2
+            for (int c = 0; c < CPR / 2; ++c) {
+                const float4 kv = *reinterpret_cast<const float4*>(kb + key * ROWB + (((hf * (CPR / 2) + c) ^ (key & 7)) << 4));
+#pragma unroll
+                for (int g = 0; g < kRows; g += 4) {
+                    if (g < nrows) {
+#pragma unroll
+                        for (int r = g; r < g + 4; ++r) {
+                            const float4 qv = *reinterpret_cast<const float4*>(s_q + (r * 2 + hf) * Gm::QH + c * 4);
+                            x[r] = fmaf(qv.x, kv.x, x[r]);
+                            x[r] = fmaf(qv.y, kv.y, x[r]);
+                            x[r] = fmaf(qv.z, kv.z, x[r]);
+                            x[r] = fmaf(qv.w, kv.w, x[r]);
+                        }
+                    }
+                }
+            }
+            // ---- softmax ----------------------------------------------------------
+            __syncwarp();
+#pragma unroll
+            for (int g = 0; g < kRows; g += 4) {
+                if (g < nrows) {
+#pragma unroll
+                    for (int r = g; r < g + 4; ++r) {
+                        x[r] += __shfl_xor_sync(0xFFFFFFFFu, x[r], 16);
+                        if constexpr (MOD) x[r] = mod.apply(x[r], s_slope[r], j - s_pos[r]);
+                        else x[r] *= mod.pre;
+                        if (!full && (j < s_lo[r] || j >= s_hi[r])) x[r] = -INFINITY;
+                        float mx = x[r];
+#pragma unroll
+                        for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, w));
+                        mx = fmaxf(mx, m[r]);
+                        const float base = mx == -INFINITY ? 0.0f : mx;
+                        if (mx > m[r]) {
+                            const float f = ex2(m[r] - base);
+                            l[r] *= f;
+#pragma unroll
+                            for (int u = 0; u < VEC; ++u) o[r][u] *= f;
+                            m[r] = mx;
+                        }
+                        const float e = ex2(x[r] - base);
+                        l[r] += e;                       // keys are held twice: halved at the end
+                        if (hf == 0) s_p[warp][r][key] = e;
+                    }
+                }
+            }
+            __syncwarp();
+            // ---- O += P V: lane = dims ---------------------------------------------
+#pragma unroll 1
+            for (int k4 = 0; k4 < 16; k4 += 4) {
+                float v[4][VEC];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const unsigned char* row = vb + (k4 + k) * ROWB;
+                    if constexpr (VEC == 2) {
+                        const float2 f = *reinterpret_cast<const float2*>(row + (((lane >> 1) ^ ((k4 + k) & 7)) << 4) + (lane & 1) * 8);
+                        v[k][0] = f.x; v[k][1] = f.y;
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < VEC; u += 4) {
+                            const float4 f = *reinterpret_cast<const float4*>(row + (((lane + u * 8) ^ ((k4 + k) & 7)) << 4));
+                            v[k][u] = f.x; v[k][u + 1] = f.y; v[k][u + 2] = f.z; v[k][u + 3] = f.w;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int g = 0; g < kRows; g += 4) {
+                    if (g < nrows) {
+#pragma unroll
+                        for (int r = g; r < g + 4; ++r) {
+                            const float4 w = *reinterpret_cast<const float4*>(&s_p[warp][r][k4]);
+                            const float pw[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                // a key the row does not see takes no part, whatever its value holds
+                                if (full || (j0 + k4 + k >= s_lo[r] && j0 + k4 + k < s_hi[r])) {
+#pragma unroll
+                                    for (int u = 0; u < VEC; ++u) o[r][u] = fmaf(pw[k], v[k][u], o[r][u]);
+                                }
+                            }
+                        }
+                    }
+                }
+            }
+        }
+        cp_wait<0>();
+        __syncthreads();
+
+        // ---- the warps' results meet in the ring ------------------------------
+        float* red = reinterpret_cast<float*>(ring);            // [warp][row][DP]
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+            for (int w = 8; w > 0; w >>= 1) l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], w);
+            if (lane == 0) { s_m[warp][r] = m[r]; s_l[warp][r] = l[r]; }
+            float* d = red + (warp * kRows + r) * DP;
+            if constexpr (VEC == 2) {
+                *reinterpret_cast<float2*>(d + lane * 2) = make_float2(o[r][0], o[r][1]);
+            } else {
+#pragma unroll
+                for (int u = 0; u < VEC; u += 4)
+                    *reinterpret_cast<float4*>(d + (lane + u * 8) * 4) = make_float4(o[r][u], o[r][u + 1], o[r][u + 2], o[r][u + 3]);
+            }
+        }
+        __syncthreads();
+        const bool part = sc.shared();
+        float* slot_o = part ? attn_slot(p, blockIdx.x, sc.w0 >= sc.us ? 0 : 1, kRows) : nullptr;
+        auto store = [&](int r, int d, float4 v, float mm, float ll) {
+            const int pr = rbase + r, ti = pr / p.G, h = sc.h * p.G + pr - ti * p.G;
+            const long long row = s.t0 + ti;
+            if (ll == 0.0f) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+            float* to = static_cast<float*>(p.out) + row * p.o_ts + (long long)h * p.o_hs + d;
+            to[0] = v.x * inv; to[1] = v.y * inv; to[2] = v.z * inv; to[3] = v.w * inv;
+            if (d == 0 && p.lse) p.lse[row * p.Hq + h] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+        };
+        for (int x = threadIdx.x; x < nrows * (DP / 4); x += NTH) {
+            const int r = x / (DP / 4), d = (x % (DP / 4)) * 4;
+            if (d >= p.D) continue;
+            float mm = s_m[0][r];
+#pragma unroll
+            for (int w = 1; w < WARPS; ++w) mm = fmaxf(mm, s_m[w][r]);
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float ll = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) {
+                const float f = part_weight(s_m[w][r], s_l[w][r], mm);
+                const float4 u = *reinterpret_cast<const float4*>(red + (w * kRows + r) * DP + d);
+                v.x = fmaf(u.x, f, v.x); v.y = fmaf(u.y, f, v.y); v.z = fmaf(u.z, f, v.z); v.w = fmaf(u.w, f, v.w);
+                ll = fmaf(s_l[w][r], f, ll);
+            }
+            if (part) {
+                __stcg(reinterpret_cast<float4*>(slot_o + r * p.D + d), v);
+                if (d == 0) { __stcg(slot_o + kRows * p.D + r, mm); __stcg(slot_o + kRows * p.D + kRows + r, ll); }
+            } else {
+                store(r, d, v, mm, ll);
+            }
+        }
+        if (part && attn_arrive(p, sc, &s_flag)) attn_join<NTH>(p, sc, nrows, ring, store);
+        __syncthreads();
+        sc.next(p);
+    }
+}
+
+template <int DP, bool MOD> cudaError_t launch_dm(const AttnParams& p, cudaStream_t st) {
+    using Gm = F32Geom<DP>;
+    static std::atomic<unsigned> configured{0};
+    auto kern = attn_f32_kernel<DP, MOD>;
+    int shift = -1;
+    if ((p.page & (p.page - 1)) == 0)
+        for (shift = 0; (1 << shift) < p.page; ++shift) {}
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned bit = 1u << (dev & 31);
+    if (!(configured.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Gm::SMEM);
+        if (e != cudaSuccess) return e;
+        configured.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(std::min(api_sms(), 148) * Gm::PER_SM));
+    cfg.blockDim = dim3(Gm::WARPS * 32);
+    cfg.dynamicSmemBytes = Gm::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p, shift);
+}
+
+template <int DP> cudaError_t launch_d(const AttnParams& p, cudaStream_t st) {
+    return p.softcap > 0.0f || p.slopes ? launch_dm<DP, true>(p, st) : launch_dm<DP, false>(p, st);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_f32(const AttnParams& p, cudaStream_t st) {
+    return p.D <= 64 ? launch_d<64>(p, st) : p.D <= 128 ? launch_d<128>(p, st) : launch_d<256>(p, st);
+}
+
+}  // namespace qmv

@@ -125,6 +125,7 @@ inline cudaError_t launch_dependent(Kern kern, std::atomic<unsigned>& configured
 cudaError_t launch_rope(int dtype, const RopeParams& p, int vec_bytes, cudaStream_t st);
 cudaError_t launch_attn_few(int dtype, const AttnParams& p, cudaStream_t st);
 cudaError_t launch_attn_chunk(int dtype, const AttnParams& p, cudaStream_t st);
+cudaError_t launch_attn_f32(const AttnParams& p, cudaStream_t st);
 cudaError_t launch_attn_rows(int dtype, const AttnParams& p, cudaStream_t st);
 
 }  // namespace qmv

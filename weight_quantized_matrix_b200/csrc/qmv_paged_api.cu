@@ -234,8 +234,10 @@ int qmv_paged_attention(const void* q, const qmv_paged_kv* kv, void* out, float*
                                 q_head_stride * (long long)eb, kv->page_stride * (long long)eb,
                                 kv->token_stride * (long long)eb, kv->head_stride * (long long)eb, D * (long long)eb});
     // whose places (in 16 bytes) fit an int: caches of up to 32 GiB a tensor
-    const bool near = (kv->n_pages - 1LL) * kv->page_stride + (kv->page_size - 1LL) * kv->token_stride <= (8LL << 31) - 8;
-    if (kv->dtype != QMV_F32 && vec == 16 && near) {
+    const long long per16 = 16 / (long long)eb;
+    const bool near = (kv->n_pages - 1LL) * kv->page_stride + (kv->page_size - 1LL) * kv->token_stride <= (per16 << 31) - per16;
+    if (vec == 16 && near && kv->dtype == QMV_F32) return qmv::api_finish(qmv::launch_attn_f32(p, s));
+    if (vec == 16 && near) {
         p.fault = qmv::api_fault_word();
         if (!p.fault) return QMV_ECUDA;
         const long long rows = (long long)(max_q_len > 0 && max_q_len < T ? max_q_len : T) * p.G;
