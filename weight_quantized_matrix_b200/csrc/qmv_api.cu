@@ -796,6 +796,8 @@ namespace qmv {
 int api_finish(cudaError_t e) { return finish(e); }
 int api_sms() { return device_sms(); }
 unsigned* api_fault_word() { return fault_word(); }
+bool api_encode_pages(CUtensorMap* m, const void* base, bool f16, int D, int page, int heads, int pages, long long tok_s,
+                      long long head_s, long long page_s, int rows);
 }  // namespace qmv
 
 namespace {
@@ -864,6 +866,25 @@ bool encode_rows_map_sw128(CUtensorMap* m, const void* base, long long row_bytes
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+}  // namespace
+
+// A paged cache of 16-bit elements, dims (D, row, head, page), boxes of 64 dims
+// (128 swizzled bytes) x `rows` rows.
+bool qmv::api_encode_pages(CUtensorMap* m, const void* base, bool f16, int D, int page, int heads, int pages,
+                           long long tok_s, long long head_s, long long page_s, int rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)page, (cuuint64_t)heads, (cuuint64_t)pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)tok_s * 2, (cuuint64_t)head_s * 2, (cuuint64_t)page_s * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
+               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
 
 // [batch][N][K/G] scales (or biases) as a 3-D tensor map with box
 // {box0 groups, rows, 1}; out-of-range elements read as zero.

@@ -14,8 +14,11 @@
 //              swizzle), O_h += P_h V (A tensor memory, B shared, V as it
 //              lies: dims contiguous, the MN-major form).  While one half's
 //              softmax runs, the tensor cores do the other half's products.
-//   warps 9-11 copy Q, K and V with cp.async, 16 bytes at a time: any page size,
-//              order and stride; keys no row sees become zeros.
+//   warps 9-11 copy K and V: tiles all of whose keys are seen by some row go by
+//              tensor copies, one a page (or 128 rows) and 64 dims, where pages are
+//              powers of two from 8 up; other pages, and the tiles at the ends,
+//              go by cp.async, 16 bytes at a time, with zeros for keys no row
+//              sees.  Q goes by cp.async.
 // Tensor memory: S_0 S_1 (128 columns each, P_h in the lower half of S_h), O_0 O_1.
 // K and V tiles of 128 keys alternate in a ring of 5 slots.
 //
@@ -63,6 +66,13 @@ struct Bars {
     int flag[2];
 };
 
+struct ChunkArgs {
+    CUtensorMap kmap, vmap;  // the cache as boxes of 64 dims x box_rows rows of a page
+    int box_rows;            // 0: no boxes (pages that are no power of two, or below 8 rows)
+    int page_shift;          // log2 of the page, -1 if it is no power of two
+    int out_vec;             // 16-byte stores
+};
+
 // The wait of every role: false once the block has given up.
 struct Waiter {
     Bars* b;
@@ -105,8 +115,8 @@ __device__ __forceinline__ void half_tiles(const AttnParams& p, const SeqInfo& s
 }
 
 template <class T, int DP, bool MOD>
-__global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_constant__ AttnParams p, int page_shift,
-                                                                 int out_vec) {
+__global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_constant__ AttnParams p,
+                                                                 const __grid_constant__ ChunkArgs g) {
     using Gm = ChunkGeom<DP>;
     constexpr int CPR = DP / 8, SLOTS = Gm::SLOTS;
     extern __shared__ unsigned char raw[];
@@ -136,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     tc_before();
     __syncthreads();
     tc_after();
-    const uint32_t tm = bars.tmem;
+    constexpr uint32_t tm = 0;                   // all 512 columns: tensor memory's start
 
     Sched<kRows, kTile> sc;
     sc.init<kThreads, 32>(p, sm, 4);
@@ -145,83 +155,85 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         reg_dec<kOtherRegs>();
         if (warp == 8) {
             // ------------------------------------------------ the products ----
-            if (lane == 0) {
-                Waiter wait{&bars, p.fault, 8u, true};
-                constexpr uint32_t FMT = __is_same(T, __half) ? 0u : 1u;
-                constexpr uint32_t ID_S = (1u << 4) | (FMT << 7) | (FMT << 10) | ((kTile / 8u) << 17) | (8u << 24);
-                constexpr uint32_t ID_O = (1u << 4) | (FMT << 7) | (FMT << 10) | (1u << 16) | ((DP / 8u) << 17) | (8u << 24);
-                int n = 0;                              // tiles of K and V taken from the ring so far
-                int npiece = 0;
-                int pv[2] = {0, 0}, pf[2] = {0, 0};      // products O and weights P so far
-                auto slot_of = [&](int x) { return x % SLOTS; };
-                auto full = [&](int x) { return wait(bars.kv_full[x % SLOTS], (uint32_t)(x / SLOTS) & 1u); };
-                auto qk = [&](int h, int x) {
-                    const uint32_t a = q_a + h * Gm::QB, b = ring_a + slot_of(x) * Gm::SLOT;
+            // The whole warp walks through this with the same values, so that
+            // descriptors live in uniform registers; one lane issues.  (With one
+            // lane in the loop alone the issue took 150 clocks a product.)
+            Waiter wait{&bars, p.fault, 8u, true};
+            constexpr uint32_t FMT = __is_same(T, __half) ? 0u : 1u;
+            constexpr uint32_t ID_S = (1u << 4) | (FMT << 7) | (FMT << 10) | ((kTile / 8u) << 17) | (8u << 24);
+            constexpr uint32_t ID_O = (1u << 4) | (FMT << 7) | (FMT << 10) | (1u << 16) | ((DP / 8u) << 17) | (8u << 24);
+            const uint32_t q_d = desc_lo(q_a, 16), ring_k = desc_lo(ring_a, 16), ring_v = desc_lo(ring_a, 128 * 128);
+            constexpr uint32_t HI = desc_hi(1024);
+            const bool one = elect_one();
+            int n = 0;                              // tiles of K and V taken from the ring so far
+            int npiece = 0;
+            int pv[2] = {0, 0}, pf[2] = {0, 0};      // products O and weights P so far
+            auto full = [&](int x) { return warp_wait(wait, bars.kv_full[x % SLOTS], (uint32_t)(x / SLOTS) & 1u); };
+            auto release = [&](int x) { if (one) commit(&bars.kv_empty[x % SLOTS]); };
+            auto qk = [&](int h, int x) {
+                // S_h is free once the product that read its weights is done
+                if (pv[h] > 0 && !warp_wait(wait, bars.pv_done[h], (uint32_t)(pv[h] - 1) & 1u)) return;
+                tc_after();
+                const uint32_t a = q_d + h * (Gm::QB / 16), b = ring_k + x % SLOTS * (Gm::SLOT / 16);
+                if (one) {
 #pragma unroll
                     for (int k = 0; k < DP / 16; ++k) {
-                        const uint32_t o = (k / 4) * (128 * 128) + (k % 4) * 32;
-                        mma_ss(tm + h * 128, desc128(a + o, 16, 1024), desc128(b + o, 16, 1024), ID_S, k > 0);
+                        const uint32_t o = ((k / 4) * (128 * 128) + (k % 4) * 32) / 16;
+                        mma_ss(h * 128, a + o, b + o, HI, ID_S, k > 0);
                     }
                     commit(&bars.s_full[h]);
-                };
-                while (sc.live && wait.ok) {
-                    int k0, k1, a[2], b[2];
-                    sc.piece(k0, k1);
-                    for (int h = 0; h < 2; ++h) half_tiles(p, sc.s, sc.i * kRows, h, k0, k1, a[h], b[h]);
-                    if (k0 < k1) {
-                        if (!wait(bars.q_full, (uint32_t)npiece & 1u)) break;
-                        if (!full(2 * n)) break;
-                        tc_after();
-                        for (int h = 0; h < 2; ++h)
-                            if (a[h] <= k0 && k0 < b[h]) {
-                                if (pv[h] > 0 && !wait(bars.pv_done[h], (uint32_t)(pv[h] - 1) & 1u)) break;
+                }
+            };
+            while (sc.live && wait.ok) {
+                int k0, k1, a[2], b[2];
+                sc.piece(k0, k1);
+                for (int h = 0; h < 2; ++h) half_tiles(p, sc.s, sc.i * kRows, h, k0, k1, a[h], b[h]);
+                if (k0 < k1) {
+                    if (!warp_wait(wait, bars.q_full, (uint32_t)npiece & 1u)) break;
+                    if (!full(2 * n)) break;
+                    tc_after();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (a[h] <= k0 && k0 < b[h]) qk(h, 2 * n);
+                    release(2 * n);
+                    if (k1 - k0 == 1 && one) commit(&bars.q_empty);
+                    for (int j = k0; j < k1; ++j, ++n) {
+                        const bool more = j + 1 < k1;
+                        if (!full(2 * n + 1)) break;
+                        if (more && !full(2 * n + 2)) break;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (a[h] <= j && j < b[h]) {
+                                if (!warp_wait(wait, bars.p_full[h], (uint32_t)pf[h]++ & 1u)) break;
                                 tc_after();
-                                qk(h, 2 * n);
-                            }
-                        commit(&bars.kv_empty[slot_of(2 * n)]);
-                        if (k1 - k0 == 1) commit(&bars.q_empty);
-                        for (int j = k0; j < k1 && wait.ok; ++j, ++n) {
-                            const bool more = j + 1 < k1;
-                            if (!full(2 * n + 1)) break;
-                            bool k_here = false;
-                            for (int h = 0; h < 2; ++h) {
-                                if (a[h] <= j && j < b[h]) {
-                                    if (!wait(bars.p_full[h], (uint32_t)pf[h]++ & 1u)) break;
-                                    tc_after();
-                                    if (!bars.skip[h]) {
-                                        const uint32_t v = ring_a + slot_of(2 * n + 1) * Gm::SLOT;
+                                const bool skip = *(volatile int*)&bars.skip[h] != 0;
+                                const uint32_t v = ring_v + (2 * n + 1) % SLOTS * (Gm::SLOT / 16);
+                                if (one) {
+                                    if (!skip) {
+                                        const bool acc = j > a[h];
 #pragma unroll
                                         for (int k = 0; k < kTile / 16; ++k)
-                                            mma_ts(tm + 256 + h * DP, tm + h * 128 + k * 8,
-                                                   desc128(v + k * 16 * 128, 128 * 128, 1024), ID_O, j > a[h] || k > 0);
+                                            mma_ts(256 + h * DP, h * 128 + k * 8, v + k * (16 * 128 / 16), HI, ID_O, acc || k > 0);
                                     }
                                     commit(&bars.pv_done[h]);
-                                    ++pv[h];
                                 }
-                                if (more && a[h] <= j + 1 && j + 1 < b[h]) {
-                                    if (!k_here && !full(2 * n + 2)) break;
-                                    k_here = true;
-                                    if (pv[h] > 0 && !wait(bars.pv_done[h], (uint32_t)(pv[h] - 1) & 1u)) break;
-                                    tc_after();
-                                    qk(h, 2 * n + 2);
-                                }
+                                ++pv[h];
                             }
-                            if (!wait.ok) break;
-                            if (more && !k_here && !full(2 * n + 2)) break;
-                            commit(&bars.kv_empty[slot_of(2 * n + 1)]);
-                            if (more) commit(&bars.kv_empty[slot_of(2 * n + 2)]);
-                            if (j + 2 == k1) commit(&bars.q_empty);
+                            if (more && a[h] <= j + 1 && j + 1 < b[h]) qk(h, 2 * n + 2);
                         }
-                        ++npiece;
+                        if (!wait.ok) break;
+                        release(2 * n + 1);
+                        if (more) release(2 * n + 2);
+                        if (j + 2 == k1 && one) commit(&bars.q_empty);
                     }
-                    sc.next(p);
+                    ++npiece;
                 }
-                // nothing of this block's is in flight when it ends
-                commit(&bars.drain);
-                wait.ok = true;
-                const uint64_t t0 = now_ns();
-                while (!mbar_try_sleep(s_addr(&bars.drain), 0u) && now_ns() - t0 < kWaitNs) {}
+                if (wait.ok) sc.next(p);
             }
+            // nothing of this block's is in flight when it ends
+            if (one) commit(&bars.drain);
+            const uint64_t t0 = now_ns();
+            while (!mbar_try_sleep(s_addr(&bars.drain), 0u) && now_ns() - t0 < kWaitNs) {}
             __syncwarp();
         } else {
             // -------------------------------------------------- the copies ----
@@ -238,6 +250,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                 if (lane == 0) mbar_arrive1(&bars.kv_full[told % SLOTS]);
                 ++told;
             };
+            // boxes: pieces of box_rows rows x 64 dims, shared out over warps and lanes
+            const bool boxes = g.box_rows > 0;
+            const int pieces = boxes ? kTile / g.box_rows : 0, items = pieces * (DP / 64), item = lane * kLoaders + w;
+            const uint32_t my_bytes = (uint32_t)((items - w + kLoaders - 1) / kLoaders) * g.box_rows * 128u;
             auto tell_all = [&]() {
                 cp_wait<0>();
                 while (told < filled) tell();
@@ -258,22 +274,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                     auto place = [&](int j0, int u) -> int {
                         const int lr = u * 32 + lane, row = (w + kLoaders * (lr >> 3)) * 8 + (lr & 7), j = j0 + row;
                         if (row >= kTile || j < ulo || j >= uhi) return -1;
-                        const int e = page_shift >= 0 ? j >> page_shift : j / p.page;
+                        const int e = g.page_shift >= 0 ? j >> g.page_shift : j / p.page;
                         if (e >= p.max_pages) return -2;
                         const int pg = __ldg(trow + e);
                         if ((unsigned)pg >= (unsigned)p.n_pages) return -2;
                         return pg * page16 + (j - e * p.page) * tok16;
                     };
+                    // page of this lane's piece of a tile, -1 where it must go row by row
+                    auto page_of = [&](int j0) -> int {
+                        const int x = j0 + lane * g.box_rows;
+                        if (lane >= pieces) return 0;
+                        const int e = x >> g.page_shift;
+                        if (j0 < ulo || j0 + kTile > uhi || e >= p.max_pages) return -1;
+                        const int pg = __ldg(trow + e);
+                        return (unsigned)pg < (unsigned)p.n_pages ? pg : -1;
+                    };
                     int at0 = place(k0 * kTile, 0), at1 = place(k0 * kTile, 1);
+                    int pg = boxes ? page_of(k0 * kTile) : -1;
                     // ---- queries, once the first products of the unit before are done ----
                     tell_all();
                     if (npiece > 0 && !warp_wait(wait, bars.q_empty, (uint32_t)(npiece - 1) & 1u)) break;
-                    for (int g = w; g < kRows / 8; g += kLoaders) {
-                        const int r = g * 8 + (lane & 7), pr = rbase + min(r, nrows - 1), ti = pr / p.G;
+                    for (int gr = w; gr < kRows / 8; gr += kLoaders) {
+                        const int r = gr * 8 + (lane & 7), pr = rbase + min(r, nrows - 1), ti = pr / p.G;
                         const long long off = ((long long)(s.t0 + ti) * p.q_ts + (long long)(sc.h * p.G + pr - ti * p.G) * p.q_hs) * 2;
 #pragma unroll
                         for (int u = 0; u < PER; ++u) {
-                            const int id = u * 32 + lane, rr = id / CPR, c = id % CPR, row = g * 8 + rr;
+                            const int id = u * 32 + lane, rr = id / CPR, c = id % CPR, row = gr * 8 + rr;
                             const long long o = __shfl_sync(0xFFFFFFFFu, off, rr);
                             const bool rd = row < nrows && c < chunks;
                             const uint32_t d = q_a + (row / kHalf) * Gm::QB + (c / 8) * (128 * 128) + (row % kHalf) * 128 +
@@ -289,7 +315,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                     ++npiece;
                     // ---- keys and values ------------------------------------------
                     for (int j = k0; j < k1 && wait.ok; ++j) {
-                        const int n0 = place((j + 1) * kTile, 0), n1 = place((j + 1) * kTile, 1);
+                        const bool by_box = boxes && __all_sync(0xFFFFFFFFu, pg >= 0);
+                        const int npg = boxes ? page_of((j + 1) * kTile) : -1;
+                        int n0 = 0, n1 = 0;
+                        if (!boxes || !__all_sync(0xFFFFFFFFu, npg >= 0)) {
+                            n0 = place((j + 1) * kTile, 0);
+                            n1 = place((j + 1) * kTile, 1);
+                        }
+                        const int my_pg = __shfl_sync(0xFFFFFFFFu, pg, item / (DP / 64) & 31);
                         for (int kv = 0; kv < 2; ++kv) {
                             const int slot = filled % SLOTS;
                             if (filled >= SLOTS) {
@@ -298,15 +331,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                                 if (!__all_sync(0xFFFFFFFFu, mbar_test(s_addr(&bars.kv_empty[slot]), ph))) tell_all();
                                 if (!warp_wait(wait, bars.kv_empty[slot], ph)) break;
                             }
+                            if (by_box) {
+                                tell_all();
+                                if (lane == 0) mbar_expect(&bars.kv_full[slot], my_bytes);
+                                __syncwarp();
+                                if (item < items) {
+                                    const int piece = item / (DP / 64), blk = item % (DP / 64);
+                                    box_copy(ring_a + slot * Gm::SLOT + blk * (128 * 128) + piece * g.box_rows * 128,
+                                             kv ? &g.vmap : &g.kmap, blk * 64, (j * kTile + piece * g.box_rows) & (p.page - 1),
+                                             sc.h, my_pg, &bars.kv_full[slot]);
+                                }
+                                ++filled;
+                                ++told;
+                                continue;
+                            }
                             const uint32_t base = ring_a + slot * Gm::SLOT;
                             const char* src = kv ? vl : kl;
 #pragma unroll
                             for (int gi = 0; gi < (16 + kLoaders - 1) / kLoaders; ++gi) {
-                                const int g = w + kLoaders * gi;
-                                if (g >= 16) break;
+                                const int gr = w + kLoaders * gi;
+                                if (gr >= 16) break;
 #pragma unroll
                                 for (int u = 0; u < PER; ++u) {
-                                    const int id = u * 32 + lane, rr = id / CPR, c = id % CPR, row = g * 8 + rr;
+                                    const int id = u * 32 + lane, rr = id / CPR, c = id % CPR, row = gr * 8 + rr;
                                     const int at = __shfl_sync(0xFFFFFFFFu, gi < 4 ? at0 : at1, (gi & 3) * 8 + rr);
                                     const uint32_t d = base + (c / 8) * (128 * 128) + row * 128 + (((c & 7) ^ rr) << 4);
                                     if (at == -2 && kv == 0) {
@@ -323,6 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                         }
                         at0 = n0;
                         at1 = n1;
+                        pg = npg;
                     }
                 }
                 sc.next(p);
@@ -523,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                             for (int u = 0; u < 16; u += 4)
                                 if (c + u < p.D) __stcg(reinterpret_cast<float4*>(d + u), make_float4(o[u], o[u + 1], o[u + 2], o[u + 3]));
                         } else {
-                            put16<T>(out + c, o, inv, p.D - c, out_vec);
+                            put16<T>(out + c, o, inv, p.D - c, g.out_vec);
                         }
                     }
                 }
@@ -577,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
 #pragma unroll
                                     for (int u = 0; u < 16; ++u) o[u] = 0.0f;
                                 }
-                                put16<T>(out + d, o, L == 0.0f ? 0.0f : 1.0f / L, p.D - d, out_vec);
+                                put16<T>(out + d, o, L == 0.0f ? 0.0f : 1.0f / L, p.D - d, g.out_vec);
                             }
                             if (p.lse) p.lse[row * p.Hq + head] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
                         }
@@ -604,10 +652,19 @@ template <class T, int DP, bool MOD> cudaError_t launch_tdm(const AttnParams& p,
     using Gm = ChunkGeom<DP>;
     static std::atomic<unsigned> configured{0};
     auto kern = attn_chunk_kernel<T, DP, MOD>;
-    int shift = -1;
+    ChunkArgs g = {};
+    g.page_shift = -1;
     if ((p.page & (p.page - 1)) == 0)
-        for (shift = 0; (1 << shift) < p.page; ++shift) {}
-    const int out_vec = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.o_ts * 2) | (uintptr_t)(p.o_hs * 2)) & 15) == 0;
+        for (g.page_shift = 0; (1 << g.page_shift) < p.page; ++g.page_shift) {}
+    g.out_vec = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.o_ts * 2) | (uintptr_t)(p.o_hs * 2)) & 15) == 0;
+    // pages of 8 rows or more, a power of two: whole pieces by tensor copies
+    if (g.page_shift >= 3) {
+        const bool f16 = __is_same(T, __half);
+        const int rows = std::min(p.page, kTile);
+        if (api_encode_pages(&g.kmap, p.k, f16, p.D, p.page, p.Hkv, p.n_pages, p.tok_s, p.head_s, p.page_s, rows) &&
+            api_encode_pages(&g.vmap, p.v, f16, p.D, p.page, p.Hkv, p.n_pages, p.tok_s, p.head_s, p.page_s, rows))
+            g.box_rows = rows;
+    }
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -631,7 +688,7 @@ template <class T, int DP, bool MOD> cudaError_t launch_tdm(const AttnParams& p,
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p, shift, out_vec);
+    return cudaLaunchKernelEx(&cfg, kern, p, g);
 }
 
 template <class T, int DP> cudaError_t launch_td(const AttnParams& p, cudaStream_t st) {

@@ -5,6 +5,7 @@
 
 #include <atomic>
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -16,6 +17,8 @@ namespace qmv {
 int api_finish(cudaError_t e);      // QMV_OK, or QMV_ECUDA (recorded for qmv_last_cuda_error)
 int api_sms();                      // multiprocessors of the current device
 unsigned* api_fault_word();         // fault word of the current device, null if unknown
+bool api_encode_pages(CUtensorMap* m, const void* base, bool f16, int D, int page, int heads, int pages, long long tok_s,
+                      long long head_s, long long page_s, int rows);
 
 // Rotation and append: rows of heads, `n_rot` rotated ones first.
 struct RopeParams {
