@@ -2,25 +2,26 @@
 // head (chunks of new tokens): 16-bit types, heads of up to 128 dims, on the
 // 5th-generation tensor cores.
 //
-// Bound by the products (4 D flops a pair of row and key) and, at the same size, by
-// the exponentials (one a pair: 16 a clock and SM, so a 128 x 128 tile takes
-// 1024 clocks, as its two products do at D = 128; at D = 64 twice as long).
+// Bound by the products (4 D flops a pair of row and key) and, at nearly the same
+// size, by the exponentials (one a pair, 16 a clock and SM: a 128 x 64 tile
+// takes 512 clocks, as its two products do at D = 128; at D = 64 they take half).
 //
-// One block an SM, 384 threads; a unit is 256 packed rows in two halves of 128:
+// One block an SM, 512 threads; a unit is 256 packed rows in two halves of 128:
 //   warps 0-3, 4-7  softmax of half 0 / 1: thread = row.  S is read from tensor
-//              memory (tcgen05.ld), the weights are written back over it in the
-//              element type as the second product's A operand.
-//   warp 8     lane 0 issues tcgen05.mma: S_h = Q_h K^T (A, B shared, 128-byte
-//              swizzle), O_h += P_h V (A tensor memory, B shared, V as it
-//              lies: dims contiguous, the MN-major form).  While one half's
-//              softmax runs, the tensor cores do the other half's products.
-//   warps 9-11 copy K and V: tiles all of whose keys are seen by some row go by
-//              tensor copies, one a page (or 128 rows) and 64 dims, where pages are
+//              memory (tcgen05.ld) and given back at once; the weights go to
+//              tensor memory in the element type as the second product's A.
+//   warps 8, 9 one lane each issues the half's tcgen05.mma: S = Q K^T (A, B
+//              shared, 128-byte swizzle), O += P V (A tensor memory, B shared, V as
+//              it lies: dims contiguous, the MN-major form).  The next step's S
+//              is made while this step's exponentials run.
+//   warps 12-15 copy K and V: tiles all of whose keys are seen by some row go by
+//              tensor copies, one a page (or 64 rows) and 64 dims, where pages are
 //              powers of two from 8 up; other pages, and the tiles at the ends,
 //              go by cp.async, 16 bytes at a time, with zeros for keys no row
 //              sees.  Q goes by cp.async.
-// Tensor memory: S_0 S_1 (128 columns each, P_h in the lower half of S_h), O_0 O_1.
-// K and V tiles of 128 keys alternate in a ring of 5 slots.
+//   warp 10    hands the block's units out, one after the other.
+// Tensor memory: S_0, S_1 (64 columns each), 2 x P_0, 2 x P_1 (32 each), O_0, O_1.
+// K and V tiles of 64 keys alternate in a ring.
 //
 // The running maximum is only raised when a row's new maximum exceeds it by 2^8:
 // softmax is invariant to the reference that is subtracted, and with a slack of
@@ -30,7 +31,7 @@
 // sum is not: an error of the size of the output's own rounding.
 //
 // Every wait is bounded (about one second); one that runs out ORs a code into
-// the fault word (1: softmax, 2: copies, 8: products), raises a flag that ends
+// the fault word (1: softmax, 2: copies, 8: products, 16: scheduling), raises a flag that ends
 // every other wait, and the block frees its tensor memory and ends.
 #include <limits.h>
 
@@ -43,27 +44,43 @@ namespace qmv {
 
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kRows = 256, kHalf = 128;
-constexpr int kTile = 128;
-constexpr int kLoaders = 3;                  // warps
-constexpr int kSoftRegs = 216, kOtherRegs = 72;      // 256 x 216 + 128 x 72 = 384 x 168
+constexpr int kTile = 64;
+constexpr int kLoaders = 4;                  // warps
+constexpr int kSoftRegs = 176, kOtherRegs = 80;      // 256 x 176 + 256 x 80 = 512 x 128
 constexpr float kSlack = 8.0f;               // log2
 
 template <int DP> struct ChunkGeom {
     static constexpr int SLOT = kTile * DP * 2;                 // bytes of a K or V tile
-    static constexpr int SLOTS = DP == 64 ? 8 : 5;
+    static constexpr int SLOTS = DP == 64 ? 16 : 10;
     static constexpr int QB = kHalf * DP * 2;                   // bytes of half a unit's queries
     static constexpr int RING = 2 * QB;                         // ring's place
     static constexpr int SMEM = RING + SLOTS * SLOT + 1024;     // slack to round the base up to 1024
 };
 
+// One unit, or this block's part of it, as the scheduling warp hands it out.
+struct Piece {
+    int live;                // 0: no more
+    int t0, n, len;          // the sequence: first row, new tokens, keys
+    int b, h, rbase;         // sequence, kv head, first packed row
+    int k0, k1;              // key tiles
+    int ulo, uhi;            // keys that any row sees
+    int a[2], e[2];          // key tiles of each half
+    int plo[2], phi[2];      // keys that every row of a half sees
+    int shared;              // other blocks have parts of the unit
+    int slot;                // this block's partial result
+    int c0, c1, slot0;       // first and last block of the unit; the first one's partial result
+};
+constexpr int kPieces = 4;
+constexpr int kReaders = 2 + kLoaders + 8;   // warps that read a piece
+
 struct Bars {
-    uint64_t kv_full[8], kv_empty[8], q_full, q_empty, s_full[2], p_full[2], pv_done[2], drain;
+    uint64_t kv_full[16], kv_empty[16], q_full, q_empty, s_full[2], s_empty[2], p_full[2][2], pv_done[2][2], drain[2];
+    uint64_t pc_full[kPieces], pc_empty[kPieces];
     uint32_t tmem;
     volatile int abort;
-    int skip[2];             // this step's second product was done by the softmax warps
-    int flag[2];
+    int skip[2][2];          // the second product was done by the softmax warps
 };
 
 struct ChunkArgs {
@@ -79,39 +96,71 @@ struct Waiter {
     unsigned* fault;
     unsigned code;
     bool ok;
-    __device__ __forceinline__ bool operator()(const uint64_t& bar, uint32_t parity) {
-        if (!ok) return false;
-        const uint32_t a = s_addr(&bar);
-        if (mbar_try_sleep(a, parity)) return true;
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) {
+        if (mbar_try_sleep(bar, parity)) return true;
         const uint64_t t0 = now_ns();
-        for (;;) {
-            if (mbar_try_sleep(a, parity)) return true;
+        while (ok) {
+            if (mbar_try_sleep(bar, parity)) return true;
             if (b->abort || now_ns() - t0 > kWaitNs) {
                 if (!b->abort && fault) atomicOr(fault, code);
                 b->abort = 1;
-                return ok = false;
+                ok = false;
             }
         }
+        return false;
     }
 };
 
-// The same for a whole warp, with one answer.
-__device__ __forceinline__ bool warp_wait(Waiter& w, const uint64_t& bar, uint32_t parity) {
+// The same for a whole warp, with one answer.  The warp is converged after it, as
+// the .aligned tcgen05 instructions that follow need it to be: lanes leave the
+// polling loop one by one, and neither a vote nor a shuffle brings them back
+// into step.
+__device__ __forceinline__ bool warp_wait_all(Waiter& w, uint32_t bar, uint32_t parity) {
     const bool r = w(bar, parity);
-    return w.ok = __all_sync(0xFFFFFFFFu, r);
+    w.ok = __all_sync(0xFFFFFFFFu, r) && w.ok;
+    __syncwarp();
+    return w.ok;
 }
 
-// Key tiles of half h inside the unit's piece [k0, k1).
-__device__ __forceinline__ void half_tiles(const AttnParams& p, const SeqInfo& s, int rbase, int h, int k0, int k1, int& a,
-                                           int& b) {
-    const int r0 = rbase + h * kHalf, r1 = min(r0 + kHalf, s.n * p.G) - 1;
-    a = b = k0;
-    if (r0 > r1) return;
-    int lo, hi;
-    rows_keys(p, s, r0, r1, lo, hi);
-    a = max(k0, lo / kTile);
-    b = min(k1, (hi + kTile - 1) / kTile);
-    if (a >= b) a = b = k0;
+// O += P V of one tile for this thread's row, key by key: keys [lo, hi) of the
+// tile are the ones the row sees.
+template <class T, int DP>
+__device__ __forceinline__ void add_by_hand(uint32_t to, uint32_t tp, const unsigned char* v, bool acc, int lo, int hi) {
+#pragma unroll 1
+    for (int c = 0; c < DP; c += 16) {
+        float o[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) o[u] = 0.0f;
+        __syncwarp();
+        if (acc) { tm_ld16(to + c, o); tm_wait_ld(); }
+#pragma unroll 1
+        for (int k = 0; k < kTile; ++k) {
+            uint32_t w2;
+            __syncwarp();
+            tm_ld1(tp + k / 2, w2);
+            tm_wait_ld();
+            const float2 pw = unpack2<T>(w2);
+            if (k >= lo && k < hi) {
+                const float pe = k & 1 ? pw.y : pw.x;
+#pragma unroll
+                for (int u = 0; u < 16; u += 8) {
+                    const int ch = (c + u) / 8;
+                    const uint4 vv = *reinterpret_cast<const uint4*>(v + (ch / 8) * (kTile * 128) + k * 128 +
+                                                                     (((ch & 7) ^ (k & 7)) << 4));
+                    const uint32_t vw[4] = {vv.x, vv.y, vv.z, vv.w};
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const float2 f2 = unpack2<T>(vw[t]);
+                        o[u + 2 * t] = fmaf(pe, f2.x, o[u + 2 * t]);
+                        o[u + 2 * t + 1] = fmaf(pe, f2.y, o[u + 2 * t + 1]);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        tm_st16(to + c, reinterpret_cast<uint32_t*>(o));
+        tm_wait_st();
+    }
 }
 
 template <class T, int DP, bool MOD>
@@ -122,24 +171,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     extern __shared__ unsigned char raw[];
     unsigned char* smem = raw + ((1024u - (s_addr(raw) & 1023u)) & 1023u);
     __shared__ Bars bars;
+    __shared__ Piece pieces_s[kPieces];
     __shared__ SchedSmem sm;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t q_a = s_addr(smem), ring_a = q_a + Gm::RING;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < SLOTS; ++i) { mbar_init1(&bars.kv_full[i], kLoaders); mbar_init1(&bars.kv_empty[i], 1); }
+        for (int i = 0; i < SLOTS; ++i) { mbar_init1(&bars.kv_full[i], 1); mbar_init1(&bars.kv_empty[i], 2); }
         mbar_init1(&bars.q_full, kLoaders);
-        mbar_init1(&bars.q_empty, 1);
+        mbar_init1(&bars.q_empty, 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init1(&bars.s_full[i], 1);
-            mbar_init1(&bars.p_full[i], 4);
-            mbar_init1(&bars.pv_done[i], 1);
-            bars.skip[i] = 0;
+            mbar_init1(&bars.s_empty[i], 4);
+            for (int u = 0; u < 2; ++u) {
+                mbar_init1(&bars.p_full[i][u], 4);
+                mbar_init1(&bars.pv_done[i][u], 1);
+                bars.skip[i][u] = 0;
+            }
+            mbar_init1(&bars.drain[i], 1);
         }
-        mbar_init1(&bars.drain, 1);
+        for (int i = 0; i < kPieces; ++i) { mbar_init1(&bars.pc_full[i], 1); mbar_init1(&bars.pc_empty[i], kReaders); }
         bars.abort = 0;
         fence_mbar_init();
     }
+    __syncwarp();
     if (warp == 8) tm_alloc(s_addr(&bars.tmem), 512);
     grid_dependency_wait();
     grid_launch_dependents();
@@ -149,154 +204,220 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     constexpr uint32_t tm = 0;                   // all 512 columns: tensor memory's start
 
     Sched<kRows, kTile> sc;
-    sc.init<kThreads, 32>(p, sm, 4);
+    sc.template init<kThreads, 32>(p, sm, 8);
 
+    // Pieces are read in order by every role but the scheduling warp: take()
+    // waits for the next one, done() gives it back.
+    int np = 0;
+    auto take = [&](Waiter& w) -> const Piece* {
+        if (!warp_wait_all(w, s_addr(&bars.pc_full[np % kPieces]), (uint32_t)(np / kPieces) & 1u)) return nullptr;
+        const Piece* pc = &pieces_s[np % kPieces];
+        return pc->live ? pc : nullptr;
+    };
+    auto done = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive1(&bars.pc_empty[np % kPieces]);
+        ++np;
+    };
+
+    __syncwarp();
     if (warp >= 8) {
         reg_dec<kOtherRegs>();
-        if (warp == 8) {
+        if (warp == 10) {
+            // ---------------------------------------------- the scheduling ----
+            Waiter wait{&bars, p.fault, 16u, true};
+#pragma unroll 1
+            for (;; ++np) {
+                if (np >= kPieces &&
+                    !warp_wait_all(wait, s_addr(&bars.pc_empty[np % kPieces]), (uint32_t)(np / kPieces - 1) & 1u))
+                    break;
+                if (lane == 0) {
+                    Piece& pc = pieces_s[np % kPieces];
+                    pc.live = sc.live;
+                    if (sc.live) {
+                        const int rbase = sc.i * kRows, rows = sc.s.n * p.G;
+                        int k0, k1;
+                        sc.piece(k0, k1);
+                        pc.t0 = sc.s.t0; pc.n = sc.s.n; pc.len = sc.s.len;
+                        pc.b = sc.b; pc.h = sc.h; pc.rbase = rbase;
+                        pc.k0 = k0; pc.k1 = k1;
+                        rows_keys(p, sc.s, rbase, min(rbase + kRows, rows) - 1, pc.ulo, pc.uhi);
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+                            const int r0 = rbase + h * kHalf, r1 = min(r0 + kHalf, rows) - 1;
+                            int a = k0, e = k0, plo = 0, phi = 0;
+                            if (r0 <= r1) {
+                                int lo, hi;
+                                visible_keys(p, sc.s.len - sc.s.n + r0 / p.G, sc.s.len, lo, phi);
+                                visible_keys(p, sc.s.len - sc.s.n + r1 / p.G, sc.s.len, plo, hi);
+                                if (lo < hi) {
+                                    a = max(k0, lo / kTile);
+                                    e = min(k1, (hi + kTile - 1) / kTile);
+                                    if (a >= e) a = e = k0;
+                                }
+                            }
+                            pc.a[h] = a; pc.e[h] = e; pc.plo[h] = plo; pc.phi[h] = phi;
+                        }
+                        pc.shared = sc.shared();
+                        pc.slot = 2 * blockIdx.x + (sc.w0 >= sc.us ? 0 : 1);
+                        pc.c0 = sc.owner(sc.us);
+                        pc.c1 = sc.owner(sc.us + sc.c - 1);
+                        pc.slot0 = 2 * pc.c0 + (sc.part(pc.c0) >= sc.us ? 0 : 1);
+                    }
+                    mbar_arrive1(&bars.pc_full[np % kPieces]);
+                }
+                __syncwarp();
+                if (!sc.live) break;
+                sc.next(p);
+            }
+        } else if (warp < 10) {
             // ------------------------------------------------ the products ----
-            // The whole warp walks through this with the same values, so that
-            // descriptors live in uniform registers; one lane issues.  (With one
-            // lane in the loop alone the issue took 150 clocks a product.)
+            // One warp a half.  The whole warp walks through this with the same
+            // values and one lane issues.  These warps share their schedulers with
+            // the softmax and wait for every instruction of their own: slots,
+            // phases and descriptors are counted up, not computed.
+            const int h = warp - 8;
             Waiter wait{&bars, p.fault, 8u, true};
             constexpr uint32_t FMT = __is_same(T, __half) ? 0u : 1u;
             constexpr uint32_t ID_S = (1u << 4) | (FMT << 7) | (FMT << 10) | ((kTile / 8u) << 17) | (8u << 24);
             constexpr uint32_t ID_O = (1u << 4) | (FMT << 7) | (FMT << 10) | (1u << 16) | ((DP / 8u) << 17) | (8u << 24);
-            const uint32_t q_d = desc_lo(q_a, 16), ring_k = desc_lo(ring_a, 16), ring_v = desc_lo(ring_a, 128 * 128);
             constexpr uint32_t HI = desc_hi(1024);
+            constexpr uint32_t LBO_K = 1u << 16, LBO_V = (kTile * 128u / 16) << 16;
+            const uint32_t q_d = desc_lo(q_a + h * Gm::QB, 16), ring_d = ring_a >> 4;
+            const uint32_t ts = tm + h * 64, tp = tm + 128 + h * 64, to = tm + 256 + h * DP;
+            const uint32_t full_a = s_addr(bars.kv_full), empty_a = s_addr(bars.kv_empty), sf_a = s_addr(&bars.s_full[h]),
+                           se_a = s_addr(&bars.s_empty[h]), pf_a = s_addr(&bars.p_full[h]), pv_a = s_addr(&bars.pv_done[h]),
+                           qe_a = s_addr(&bars.q_empty);
             const bool one = elect_one();
-            int n = 0;                              // tiles of K and V taken from the ring so far
-            int npiece = 0;
-            int pv[2] = {0, 0}, pf[2] = {0, 0};      // products O and weights P so far
-            auto full = [&](int x) { return warp_wait(wait, bars.kv_full[x % SLOTS], (uint32_t)(x / SLOTS) & 1u); };
-            auto release = [&](int x) { if (one) commit(&bars.kv_empty[x % SLOTS]); };
-            auto qk = [&](int h, int x) {
-                // S_h is free once the product that read its weights is done
-                if (pv[h] > 0 && !warp_wait(wait, bars.pv_done[h], (uint32_t)(pv[h] - 1) & 1u)) return;
-                tc_after();
-                const uint32_t a = q_d + h * (Gm::QB / 16), b = ring_k + x % SLOTS * (Gm::SLOT / 16);
-                if (one) {
-#pragma unroll
-                    for (int k = 0; k < DP / 16; ++k) {
-                        const uint32_t o = ((k / 4) * (128 * 128) + (k % 4) * 32) / 16;
-                        mma_ss(h * 128, a + o, b + o, HI, ID_S, k > 0);
-                    }
-                    commit(&bars.s_full[h]);
-                }
-            };
-            while (sc.live && wait.ok) {
-                int k0, k1, a[2], b[2];
-                sc.piece(k0, k1);
-                for (int h = 0; h < 2; ++h) half_tiles(p, sc.s, sc.i * kRows, h, k0, k1, a[h], b[h]);
-                if (k0 < k1) {
-                    if (!warp_wait(wait, bars.q_full, (uint32_t)npiece & 1u)) break;
-                    if (!full(2 * n)) break;
+            // K and V of a step are slots 2 n and 2 n + 1 of the ring, which has an
+            // even number: K tiles live in even slots.
+            int ks = 0, vs = 1;                     // next slots
+            uint32_t kph = 0, vph = 0, qph = 0;     // phases of the slots, of Q
+            int sn = 0, pn = 0;                     // first and second products of this half so far
+            auto qk = [&](bool mine) {              // takes a K tile; S = Q K^T
+                wait(full_a + ks * 8, kph);
+                if (mine) {
+                    // the softmax holds the S before in registers
+                    if (sn > 0) wait(se_a, (uint32_t)(sn - 1) & 1u);
                     tc_after();
+                    if (one && wait.ok) {
+                        const uint32_t b = (ring_d + ks * (Gm::SLOT / 16)) | LBO_K;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (a[h] <= k0 && k0 < b[h]) qk(h, 2 * n);
-                    release(2 * n);
-                    if (k1 - k0 == 1 && one) commit(&bars.q_empty);
-                    for (int j = k0; j < k1; ++j, ++n) {
-                        const bool more = j + 1 < k1;
-                        if (!full(2 * n + 1)) break;
-                        if (more && !full(2 * n + 2)) break;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (a[h] <= j && j < b[h]) {
-                                if (!warp_wait(wait, bars.p_full[h], (uint32_t)pf[h]++ & 1u)) break;
-                                tc_after();
-                                const bool skip = *(volatile int*)&bars.skip[h] != 0;
-                                const uint32_t v = ring_v + (2 * n + 1) % SLOTS * (Gm::SLOT / 16);
-                                if (one) {
-                                    if (!skip) {
-                                        const bool acc = j > a[h];
-#pragma unroll
-                                        for (int k = 0; k < kTile / 16; ++k)
-                                            mma_ts(256 + h * DP, h * 128 + k * 8, v + k * (16 * 128 / 16), HI, ID_O, acc || k > 0);
-                                    }
-                                    commit(&bars.pv_done[h]);
-                                }
-                                ++pv[h];
-                            }
-                            if (more && a[h] <= j + 1 && j + 1 < b[h]) qk(h, 2 * n + 2);
+                        for (int k = 0; k < DP / 16; ++k) {
+                            const uint32_t o = (k % 4) * (32 / 16);
+                            mma_ss(ts, q_d + (k / 4) * (kHalf * 128 / 16) + o, b + (k / 4) * (kTile * 128 / 16) + o, HI, ID_S, k > 0);
                         }
-                        if (!wait.ok) break;
-                        release(2 * n + 1);
-                        if (more) release(2 * n + 2);
-                        if (j + 2 == k1 && one) commit(&bars.q_empty);
+                        commit(sf_a);
                     }
-                    ++npiece;
+                    ++sn;
                 }
-                if (wait.ok) sc.next(p);
+                if (one && wait.ok) commit(empty_a + ks * 8);
+                ks += 2;
+                if (ks == SLOTS) { ks = 0; kph ^= 1u; }
+            };
+#pragma unroll 1
+            while (const Piece* pc = take(wait)) {
+                const int k0 = pc->k0, k1 = pc->k1, a = pc->a[h], e = pc->e[h];
+                if (k0 < k1) {
+                    wait(s_addr(&bars.q_full), qph);
+                    qph ^= 1u;
+                    // first products k0 .. k1 - 1, each one step ahead of its second
+#pragma unroll 1
+                    for (int j = k0 - 1; j < k1 && wait.ok; ++j) {
+                        if (j + 1 < k1) {
+                            qk(a <= j + 1 && j + 1 < e);
+                            if (j + 2 == k1 && one) commit(qe_a);
+                        }
+                        if (j < k0) continue;
+                        wait(full_a + vs * 8, vph);
+                        if (a <= j && j < e) {
+                            const int u = pn & 1;
+                            wait(pf_a + u * 8, (uint32_t)(pn >> 1) & 1u);
+                            tc_after();
+                            if (one && wait.ok) {
+                                if (!*(volatile int*)&bars.skip[h][u]) {
+                                    const uint32_t v = (ring_d + vs * (Gm::SLOT / 16)) | LBO_V, w = tp + u * 32;
+                                    mma_ts(to, w, v, HI, ID_O, j > a);
+#pragma unroll
+                                    for (int k = 1; k < kTile / 16; ++k)
+                                        mma_ts(to, w + k * 8, v + k * (16 * 128 / 16), HI, ID_O, true);
+                                }
+                                commit(pv_a + u * 8);
+                            }
+                            ++pn;
+                        }
+                        if (one && wait.ok) commit(empty_a + vs * 8);
+                        vs += 2;
+                        if (vs > SLOTS) { vs = 1; vph ^= 1u; }
+                    }
+                }
+                done();
             }
             // nothing of this block's is in flight when it ends
-            if (one) commit(&bars.drain);
+            const uint32_t dr_a = s_addr(&bars.drain[h]);
+            if (one) commit(dr_a);
             const uint64_t t0 = now_ns();
-            while (!mbar_try_sleep(s_addr(&bars.drain), 0u) && now_ns() - t0 < kWaitNs) {}
+            while (!mbar_try_sleep(dr_a, 0u) && now_ns() - t0 < kWaitNs) {}
             __syncwarp();
-        } else {
+        } else if (warp >= kThreads / 32 - kLoaders) {
             // -------------------------------------------------- the copies ----
+            // Slot x of the ring is filled by warp x % 4 alone: a warp's K or V, every
+            // second tile.  (All four warps on each tile took 1000 clocks a slot,
+            // the time of one warp's instructions, and bound the kernel.)
             Waiter wait{&bars, p.fault, 2u, true};
-            const int w = warp - 9;
+            const int w = warp - (kThreads / 32 - kLoaders), kv = w & 1;
             const int chunks = p.D / 8;
             const int page16 = (int)(p.page_s / 8), tok16 = (int)(p.tok_s / 8);
             constexpr int PER = 8 * CPR / 32;            // copies a lane makes of 8 rows
-            constexpr int LAG = 2;                       // slots in flight behind the one being issued
-            int filled = 0, told = 0;                    // slots filled, slots reported full
+            const uint32_t full_a = s_addr(bars.kv_full), empty_a = s_addr(bars.kv_empty);
+            const int pieces = g.box_rows > 0 ? kTile / g.box_rows : 0, items = pieces * (DP / 64);
+            const CUtensorMap* map = kv ? &g.vmap : &g.kmap;
+            int slot = w, fills = 0;
+            uint32_t sph = 1;                            // a fresh barrier's phase of parity 1 is over
+            int pend = -1;                               // slot whose cp.async copies are not reported yet
             auto tell = [&]() {
                 fence_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive1(&bars.kv_full[told % SLOTS]);
-                ++told;
+                if (lane == 0) mbar_arrive1(&bars.kv_full[pend]);
+                pend = -1;
             };
-            // boxes: pieces of box_rows rows x 64 dims, shared out over warps and lanes
-            const bool boxes = g.box_rows > 0;
-            const int pieces = boxes ? kTile / g.box_rows : 0, items = pieces * (DP / 64), item = lane * kLoaders + w;
-            const uint32_t my_bytes = (uint32_t)((items - w + kLoaders - 1) / kLoaders) * g.box_rows * 128u;
-            auto tell_all = [&]() {
-                cp_wait<0>();
-                while (told < filled) tell();
+            auto flush = [&]() {
+                if (pend >= 0) { cp_wait<0>(); tell(); }
             };
-            int npiece = 0;
-            while (sc.live && wait.ok) {
-                int k0, k1;
-                sc.piece(k0, k1);
+            int npiece = 0, n0 = 0;                      // pieces and tiles before this one
+#pragma unroll 1
+            while (const Piece* pc = take(wait)) {
+                const int k0 = pc->k0, k1 = pc->k1;
                 if (k0 < k1) {
-                    const SeqInfo s = sc.s;
-                    const int rbase = sc.i * kRows, nrows = min(kRows, s.n * p.G - rbase);
-                    int ulo, uhi;
-                    rows_keys(p, s, rbase, rbase + nrows - 1, ulo, uhi);
-                    const char* kl = static_cast<const char*>(p.k) + (long long)sc.h * p.head_s * 2 + lane % CPR * 16;
-                    const char* vl = static_cast<const char*>(p.v) + (long long)sc.h * p.head_s * 2 + lane % CPR * 16;
-                    const int* trow = p.table + (long long)sc.b * p.max_pages;
-                    // this warp's rows of a tile: the 8-row groups w, w + 3, ..
-                    auto place = [&](int j0, int u) -> int {
-                        const int lr = u * 32 + lane, row = (w + kLoaders * (lr >> 3)) * 8 + (lr & 7), j = j0 + row;
-                        if (row >= kTile || j < ulo || j >= uhi) return -1;
+                    const int rbase = pc->rbase, nrows = min(kRows, pc->n * p.G - rbase), ulo = pc->ulo, uhi = pc->uhi, hk = pc->h;
+                    const char* src = static_cast<const char*>(kv ? p.v : p.k) + (long long)hk * p.head_s * 2 + lane % CPR * 16;
+                    const int* trow = p.table + (long long)pc->b * p.max_pages;
+                    // place of key j, in units of 16 bytes; -1 where no row sees it, -2 on a bad page
+                    auto place = [&](int j) -> int {
+                        if (j < ulo || j >= uhi) return -1;
                         const int e = g.page_shift >= 0 ? j >> g.page_shift : j / p.page;
                         if (e >= p.max_pages) return -2;
                         const int pg = __ldg(trow + e);
                         if ((unsigned)pg >= (unsigned)p.n_pages) return -2;
                         return pg * page16 + (j - e * p.page) * tok16;
                     };
-                    // page of this lane's piece of a tile, -1 where it must go row by row
+                    // page of this lane's box of a tile, -1 where the tile must go row by row
                     auto page_of = [&](int j0) -> int {
-                        const int x = j0 + lane * g.box_rows;
-                        if (lane >= pieces) return 0;
-                        const int e = x >> g.page_shift;
+                        if (lane >= items) return 0;
+                        const int e = (j0 + lane / (DP / 64) * g.box_rows) >> g.page_shift;
                         if (j0 < ulo || j0 + kTile > uhi || e >= p.max_pages) return -1;
                         const int pg = __ldg(trow + e);
                         return (unsigned)pg < (unsigned)p.n_pages ? pg : -1;
                     };
-                    int at0 = place(k0 * kTile, 0), at1 = place(k0 * kTile, 1);
-                    int pg = boxes ? page_of(k0 * kTile) : -1;
+                    int j = k0 + (((n0 ^ (w >> 1)) & 1));         // this warp's first tile
+                    int pg = items > 0 ? page_of(j * kTile) : -1;
                     // ---- queries, once the first products of the unit before are done ----
-                    tell_all();
-                    if (npiece > 0 && !warp_wait(wait, bars.q_empty, (uint32_t)(npiece - 1) & 1u)) break;
+                    flush();
+                    if (npiece > 0 && !warp_wait_all(wait, s_addr(&bars.q_empty), (uint32_t)(npiece - 1) & 1u)) break;
+#pragma unroll 1
                     for (int gr = w; gr < kRows / 8; gr += kLoaders) {
                         const int r = gr * 8 + (lane & 7), pr = rbase + min(r, nrows - 1), ti = pr / p.G;
-                        const long long off = ((long long)(s.t0 + ti) * p.q_ts + (long long)(sc.h * p.G + pr - ti * p.G) * p.q_hs) * 2;
+                        const long long off = ((long long)(pc->t0 + ti) * p.q_ts + (long long)(hk * p.G + pr - ti * p.G) * p.q_hs) * 2;
 #pragma unroll
                         for (int u = 0; u < PER; ++u) {
                             const int id = u * 32 + lane, rr = id / CPR, c = id % CPR, row = gr * 8 + rr;
@@ -313,133 +434,132 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                     __syncwarp();
                     if (lane == 0) mbar_arrive1(&bars.q_full);
                     ++npiece;
-                    // ---- keys and values ------------------------------------------
-                    for (int j = k0; j < k1 && wait.ok; ++j) {
-                        const bool by_box = boxes && __all_sync(0xFFFFFFFFu, pg >= 0);
-                        const int npg = boxes ? page_of((j + 1) * kTile) : -1;
-                        int n0 = 0, n1 = 0;
-                        if (!boxes || !__all_sync(0xFFFFFFFFu, npg >= 0)) {
-                            n0 = place((j + 1) * kTile, 0);
-                            n1 = place((j + 1) * kTile, 1);
-                        }
-                        const int my_pg = __shfl_sync(0xFFFFFFFFu, pg, item / (DP / 64) & 31);
-                        for (int kv = 0; kv < 2; ++kv) {
-                            const int slot = filled % SLOTS;
-                            if (filled >= SLOTS) {
-                                const uint32_t ph = (uint32_t)(filled / SLOTS - 1) & 1u;
-                                // about to wait: what is on its way is reported first
-                                if (!__all_sync(0xFFFFFFFFu, mbar_test(s_addr(&bars.kv_empty[slot]), ph))) tell_all();
-                                if (!warp_wait(wait, bars.kv_empty[slot], ph)) break;
+                    // ---- keys or values ---------------------------------------------
+#pragma unroll 1
+                    for (; j < k1; j += 2) {
+                        const uint32_t base = ring_a + slot * Gm::SLOT;
+                        if (__all_sync(0xFFFFFFFFu, pg >= 0)) {
+                            const int npg = page_of((j + 2) * kTile);
+                            flush();
+                            if (!warp_wait_all(wait, empty_a + slot * 8, sph)) break;
+                            if (lane == 0) mbar_expect(&bars.kv_full[slot], (uint32_t)Gm::SLOT);
+                            __syncwarp();
+                            if (lane < items) {
+                                const int piece = lane / (DP / 64), blk = lane % (DP / 64);
+                                box_copy(base + blk * (kTile * 128) + piece * g.box_rows * 128, map, blk * 64,
+                                         (j * kTile + piece * g.box_rows) & (p.page - 1), hk, pg, &bars.kv_full[slot]);
                             }
-                            if (by_box) {
-                                tell_all();
-                                if (lane == 0) mbar_expect(&bars.kv_full[slot], my_bytes);
-                                __syncwarp();
-                                if (item < items) {
-                                    const int piece = item / (DP / 64), blk = item % (DP / 64);
-                                    box_copy(ring_a + slot * Gm::SLOT + blk * (128 * 128) + piece * g.box_rows * 128,
-                                             kv ? &g.vmap : &g.kmap, blk * 64, (j * kTile + piece * g.box_rows) & (p.page - 1),
-                                             sc.h, my_pg, &bars.kv_full[slot]);
-                                }
-                                ++filled;
-                                ++told;
-                                continue;
-                            }
-                            const uint32_t base = ring_a + slot * Gm::SLOT;
-                            const char* src = kv ? vl : kl;
-#pragma unroll
-                            for (int gi = 0; gi < (16 + kLoaders - 1) / kLoaders; ++gi) {
-                                const int gr = w + kLoaders * gi;
-                                if (gr >= 16) break;
+                            pg = npg;
+                        } else {
+                            const int at[2] = {place(j * kTile + lane), place(j * kTile + 32 + lane)};
+                            if (items > 0) pg = page_of((j + 2) * kTile);
+                            // about to wait: what is on its way is reported first
+                            if (pend >= 0 && !__all_sync(0xFFFFFFFFu, mbar_test(empty_a + slot * 8, sph))) flush();
+                            if (!warp_wait_all(wait, empty_a + slot * 8, sph)) break;
+#pragma unroll 1
+                            for (int gr = 0; gr < kTile / 8; ++gr) {
 #pragma unroll
                                 for (int u = 0; u < PER; ++u) {
-                                    const int id = u * 32 + lane, rr = id / CPR, c = id % CPR, row = gr * 8 + rr;
-                                    const int at = __shfl_sync(0xFFFFFFFFu, gi < 4 ? at0 : at1, (gi & 3) * 8 + rr);
-                                    const uint32_t d = base + (c / 8) * (128 * 128) + row * 128 + (((c & 7) ^ rr) << 4);
-                                    if (at == -2 && kv == 0) {
+                                    const int id = u * 32 + lane, rr = id / CPR, c = id % CPR;
+                                    const int ra = __shfl_sync(0xFFFFFFFFu, gr < 4 ? at[0] : at[1], (gr & 3) * 8 + rr);
+                                    const uint32_t d = base + (c / 8) * (kTile * 128) + (gr * 8 + rr) * 128 + (((c & 7) ^ rr) << 4);
+                                    if (ra == -2 && kv == 0) {
                                         st_shared16(d, ~0u);                 // a key of NaN
                                     } else {
-                                        const bool rd = at >= 0 && c < chunks;
-                                        cp16_or_zero(d, src + (rd ? (long long)at * 16 : -16 * c), rd);
+                                        const bool rd = ra >= 0 && c < chunks;
+                                        cp16_or_zero(d, src + (rd ? (long long)ra * 16 : -16 * c), rd);
                                     }
                                 }
                             }
                             cp_commit();
-                            ++filled;
-                            if (filled - told > LAG) { cp_wait<LAG>(); tell(); }
+                            if (pend >= 0) { cp_wait<1>(); tell(); }
+                            pend = slot;
                         }
-                        at0 = n0;
-                        at1 = n1;
-                        pg = npg;
+                        ++fills;
+                        slot += 4;
+                        if (slot >= SLOTS) { slot -= SLOTS; sph ^= 1u; }
                     }
+                    n0 += k1 - k0;
                 }
-                sc.next(p);
+                done();
             }
-            tell_all();
+            cp_wait<0>();
+            if (pend >= 0) tell();
+            if (!wait.ok) {
+                // given up: this warp's tensor copies land before the block ends
+                const uint64_t t0 = now_ns();
+                for (int f = max(0, fills - (SLOTS + 3) / 4); f < fills; ++f) {
+                    const int x = w + 4 * f;
+                    while (!mbar_test(full_a + x % SLOTS * 8, (uint32_t)(x / SLOTS) & 1u) && now_ns() - t0 < kWaitNs) {}
+                }
+                __syncwarp();
+            }
         }
     } else {
         // ---------------------------------------------------- the softmax ----
+        // Nothing here waits for another warp but on the bounded barriers: a warp
+        // that gives up leaves the others free to do so.
         reg_inc<kSoftRegs>();
         const int h = warp >> 2;                         // half
         const int r = threadIdx.x & 127;                 // row of the half = lane of tensor memory
         const uint32_t lane_base = (uint32_t)(warp & 3) << 21;      // 32 lanes a warp, lane in bits 16..
-        const uint32_t ts = tm + h * 128 + lane_base, to = tm + 256 + h * DP + lane_base;
+        const uint32_t ts = tm + h * 64 + lane_base, tp0 = tm + 128 + h * 64 + lane_base, to = tm + 256 + h * DP + lane_base;
         const ScoreMod<false> mod(p);
         const float scale2 = p.scale * kLog2e;
         Waiter wait{&bars, p.fault, 1u, true};
         int ns = 0;                                      // steps of this half so far
         int n0 = 0;                                      // tiles of all pieces before this one
-        // A wait that gave up does not end these warps: they go through their
-        // steps (without waiting), so that the barriers among them stay paired.
-        while (sc.live) {
-            int k0, k1, a, b;
-            sc.piece(k0, k1);
-            const SeqInfo s = sc.s;
-            const int rbase = sc.i * kRows + h * kHalf, nrows = min(kHalf, s.n * p.G - rbase);
-            half_tiles(p, s, sc.i * kRows, h, k0, k1, a, b);
+#pragma unroll 1
+        while (const Piece* pc = take(wait)) {
+            const int k0 = pc->k0, a = pc->a[h], e = pc->e[h];
+            const int rbase = pc->rbase + h * kHalf, nrows = min(kHalf, pc->n * p.G - rbase);
             int lo = 0, hi = 0, pos = 0, ti = 0, head = 0;
             float slope = 0.0f;
             if (r < nrows) {
                 const int pr = rbase + r;
                 ti = pr / p.G;
-                head = sc.h * p.G + pr - ti * p.G;
-                pos = s.len - s.n + ti;
-                visible_keys(p, pos, s.len, lo, hi);
+                head = pc->h * p.G + pr - ti * p.G;
+                pos = pc->len - pc->n + ti;
+                visible_keys(p, pos, pc->len, lo, hi);
                 if (MOD && p.slopes) slope = __ldg(p.slopes + head) * kLog2e;
             }
-            int part_lo = 0, part_hi = 0;                // keys that every row of the half sees
-            if (nrows > 0) {
-                int x;
-                visible_keys(p, s.len - s.n + rbase / p.G, s.len, x, part_hi);
-                visible_keys(p, s.len - s.n + (rbase + nrows - 1) / p.G, s.len, part_lo, x);
-            }
+            // keys that every row of the half sees
+            const int part_lo = pc->plo[h], part_hi = pc->phi[h];
             float m = -INFINITY, l = 0.0f;
-            for (int j = a; j < b; ++j, ++ns) {
-                warp_wait(wait, bars.s_full[h], (uint32_t)ns & 1u);
+#pragma unroll 1
+            for (int j = a; j < e && wait.ok; ++j, ++ns) {
+                const int u2 = ns & 1;                   // which P of the half
+                const uint32_t tp = tp0 + u2 * 32;
+                if (!warp_wait_all(wait, s_addr(&bars.s_full[h]), (uint32_t)ns & 1u)) break;
                 tc_after();
-                float x[128];
-#pragma unroll
-                for (int c = 0; c < 128; c += 32) tm_ld32(ts + c, x + c);
-                tm_wait_ld();
+                float x[kTile];
+                tm_ld32(ts, x);
+                tm_ld32(ts + 32, x + 32);
                 const int j0 = j * kTile;
-                if constexpr (MOD) {
-#pragma unroll
-                    for (int c = 0; c < 128; ++c) x[c] = mod.apply(x[c], slope, j0 + c - pos);
-                }
                 // rows past the unit have queries of zero and need no mask
                 const bool full = __all_sync(0xFFFFFFFFu, r >= nrows || (lo <= j0 && j0 + kTile <= hi));
+                tm_wait_ld();
+                tc_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(&bars.s_empty[h]);      // the next S may be written
+                if constexpr (MOD) {
+#pragma unroll
+                    for (int c = 0; c < kTile; ++c) x[c] = mod.apply(x[c], slope, j0 + c - pos);
+                }
                 if (!full) {
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
+                    for (int c = 0; c < kTile; ++c)
                         if (j0 + c < lo || j0 + c >= hi) x[c] = -INFINITY;
                 }
-                float mx = -INFINITY;
+                float mx;
                 {
                     float mm[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                    for (int c = 4; c < 128; c += 4)
+                    for (int c = 4; c + 8 <= kTile; c += 8)
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) mm[u] = fmaxf(mm[u], x[c + u]);
+                        for (int u = 0; u < 4; ++u) mm[u] = max3(mm[u], x[c + u], x[c + 4 + u]);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) mm[u] = fmaxf(mm[u], x[kTile - 4 + u]);
                     mx = fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3]));
                 }
                 if constexpr (!MOD) mx *= scale2;
@@ -450,9 +570,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                     const float f = raise ? (m == -INFINITY ? 0.0f : ex2(m - mx)) : 1.0f;
                     if (raise) { m = mx; l *= f; }
                     if (j > a) {
-                        warp_wait(wait, bars.pv_done[h], (uint32_t)(ns - 1) & 1u);
+                        if (!warp_wait_all(wait, s_addr(&bars.pv_done[h][u2 ^ 1]), (uint32_t)((ns - 1) >> 1) & 1u)) break;
                         tc_after();
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < DP; c += 16) {
                             float o[16];
                             tm_ld16(to + c, o);
@@ -464,184 +584,157 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                         tm_wait_st();
                     }
                 }
+                // this P was last read by the second product two steps ago
+                if (ns >= 2 && !warp_wait_all(wait, s_addr(&bars.pv_done[h][u2]), (uint32_t)((ns >> 1) - 1) & 1u)) break;
+                __syncwarp();
+                tc_after();
                 const float base = m == -INFINITY ? 0.0f : m;
-                float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                const float2 nb = make_float2(-base, -base), sc2 = make_float2(MOD ? 1.0f : scale2, MOD ? 1.0f : scale2);
+                float2 ls[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-                for (int c = 0; c < 128; c += 32) {
+                for (int c = 0; c < kTile; c += 32) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int u = 0; u < 32; u += 2) {
-                        float e0, e1;
-                        if constexpr (MOD) { e0 = ex2(x[c + u] - base); e1 = ex2(x[c + u + 1] - base); }
-                        else { e0 = ex2(fmaf(x[c + u], scale2, -base)); e1 = ex2(fmaf(x[c + u + 1], scale2, -base)); }
-                        ls[(u / 2) & 1] += e0;
-                        ls[2 + ((u / 2) & 1)] += e1;
-                        pk[u / 2] = pack2<T>(e0, e1);
+                        float2 w = fma2(make_float2(x[c + u], x[c + u + 1]), sc2, nb);
+                        w.x = ex2(w.x);
+                        w.y = ex2(w.y);
+                        ls[(u / 2) & 1] = add2(ls[(u / 2) & 1], w);
+                        pk[u / 2] = pack2<T>(w.x, w.y);
                     }
-                    tm_st16(ts + c / 2, pk);
+                    tm_st16(tp + c / 2, pk);
                 }
-                l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
                 tm_wait_st();
-                // Where some rows see a key and others do not, an infinite or
-                // NaN value must not reach the others through 0 * v: these
-                // warps then add such a tile (no finite model makes one)
-                // themselves, key by key.
-                bool by_hand = false;
+                // Where some rows see a key and others do not, an infinite or NaN
+                // value must not reach the others through 0 * v: the half's warps
+                // (each finds out for itself) then add such a tile, which no
+                // finite model makes, key by key.
                 if (j0 < part_lo || j0 + kTile > part_hi) {
-                    {
-                        const int x2 = 2 * (n0 + j - k0) + 1;
-                        warp_wait(wait, bars.kv_full[x2 % SLOTS], (uint32_t)(x2 / SLOTS) & 1u);
-                        const unsigned char* v = smem + Gm::RING + (x2 % SLOTS) * Gm::SLOT;
-                        bool odd = false;
-                        for (int u = r; u < Gm::SLOT / 16; u += kHalf) {
-                            const uint4 q4 = reinterpret_cast<const uint4*>(v)[u];
-                            odd |= odd_word<T>(q4.x) || odd_word<T>(q4.y) || odd_word<T>(q4.z) || odd_word<T>(q4.w);
-                        }
-                        by_hand = bar_or(1 + h, odd);
-                        if (by_hand) {
-                            if (j > a) warp_wait(wait, bars.pv_done[h], (uint32_t)(ns - 1) & 1u);
-                            tc_after();
-                            for (int c = 0; c < DP; c += 16) {
-                                float o[16];
-                                if (j > a) { tm_ld16(to + c, o); tm_wait_ld(); }
-                                else {
-#pragma unroll
-                                    for (int u = 0; u < 16; ++u) o[u] = 0.0f;
-                                }
-                                for (int k = 0; k < kTile; k += 2) {
-                                    uint32_t w2;
-                                    tm_ld1(ts + k / 2, w2);
-                                    tm_wait_ld();
-                                    const float2 pw = unpack2<T>(w2);
-#pragma unroll
-                                    for (int e = 0; e < 2; ++e) {
-                                        const int jk = j0 + k + e;
-                                        if (jk < lo || jk >= hi) continue;
-                                        const float pe = e ? pw.y : pw.x;
-#pragma unroll
-                                        for (int u = 0; u < 16; u += 8) {
-                                            const int ch = (c + u) / 8;
-                                            const uint4 vv = *reinterpret_cast<const uint4*>(
-                                                v + (ch / 8) * (128 * 128) + (k + e) * 128 + (((ch & 7) ^ ((k + e) & 7)) << 4));
-                                            const uint32_t vw[4] = {vv.x, vv.y, vv.z, vv.w};
-#pragma unroll
-                                            for (int t = 0; t < 4; ++t) {
-                                                const float2 f2 = unpack2<T>(vw[t]);
-                                                o[u + 2 * t] = fmaf(pe, f2.x, o[u + 2 * t]);
-                                                o[u + 2 * t + 1] = fmaf(pe, f2.y, o[u + 2 * t + 1]);
-                                            }
-                                        }
-                                    }
-                                    __syncwarp();
-                                }
-                                tm_st16(to + c, reinterpret_cast<uint32_t*>(o));
-                                tm_wait_st();
-                            }
-                        }
+                    const int x2 = 2 * (n0 + j - k0) + 1;
+                    if (!warp_wait_all(wait, s_addr(&bars.kv_full[x2 % SLOTS]), (uint32_t)(x2 / SLOTS) & 1u)) break;
+                    const unsigned char* v = smem + Gm::RING + (x2 % SLOTS) * Gm::SLOT;
+                    bool odd = false;
+#pragma unroll 4
+                    for (int u = lane; u < Gm::SLOT / 16; u += 32) {
+                        const uint4 q4 = reinterpret_cast<const uint4*>(v)[u];
+                        odd |= odd_word<T>(q4.x) || odd_word<T>(q4.y) || odd_word<T>(q4.z) || odd_word<T>(q4.w);
                     }
+                    odd = __any_sync(0xFFFFFFFFu, odd);
+                    if (odd) {
+                        if (j > a && !warp_wait_all(wait, s_addr(&bars.pv_done[h][u2 ^ 1]), (uint32_t)((ns - 1) >> 1) & 1u)) break;
+                        tc_after();
+                        add_by_hand<T, DP>(to, tp, v, j > a, lo - j0, hi - j0);
+                    }
+                    if (r == 0) bars.skip[h][u2] = odd;
+                } else if (r == 0) {
+                    bars.skip[h][u2] = 0;
                 }
-                if (r == 0) bars.skip[h] = by_hand;
                 tc_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive1(&bars.p_full[h]);
+                if (lane == 0) mbar_arrive1(&bars.p_full[h][u2]);
             }
-            // ---- the half's result ---------------------------------------------
-            const bool any = b > a;
-            if (any) warp_wait(wait, bars.pv_done[h], (uint32_t)(ns - 1) & 1u);
+            if (!wait.ok) break;
+            // ---- the rows' result ----------------------------------------------
+            const bool any = e > a;
+            if (any && !warp_wait_all(wait, s_addr(&bars.pv_done[h][(ns - 1) & 1]), (uint32_t)((ns - 1) >> 1) & 1u)) break;
             tc_after();
-            const bool part = sc.shared();
-            if (nrows > 0) {
-                const bool empty = l == 0.0f;
-                const float inv = empty ? 0.0f : 1.0f / l;
-                float* so = attn_slot(p, blockIdx.x, sc.w0 >= sc.us ? 0 : 1, kRows);
-                const long long row = s.t0 + ti;
-                T* out = static_cast<T*>(p.out) + row * p.o_ts + (long long)head * p.o_hs;
+            const bool mine = r < nrows, empty = l == 0.0f, part = pc->shared;
+            const float inv = empty ? 0.0f : 1.0f / l;
+            const long long row = pc->t0 + ti;
+            T* out = static_cast<T*>(p.out) + row * p.o_ts + (long long)head * p.o_hs;
+            const size_t ss = (size_t)kRows * (p.D + 2);
+            const int at = h * kHalf + r;                // row of the unit
+            float* so = p.partials + pc->slot * ss;
+#pragma unroll 1
+            for (int c = 0; c < p.D; c += 16) {
+                float o[16];
+                __syncwarp();
+                if (any) { tm_ld16(to + c, o); tm_wait_ld(); }
+                if (empty) {
 #pragma unroll
-                for (int c = 0; c < DP; c += 16) {
-                    float o[16];
-                    if (any) { tm_ld16(to + c, o); tm_wait_ld(); }
-                    if (r < nrows && c < p.D) {
-                        if (empty) {
-#pragma unroll
-                            for (int u = 0; u < 16; ++u) o[u] = 0.0f;
-                        }
-                        if (part) {
-                            float* d = so + (size_t)(h * kHalf + r) * p.D + c;
-#pragma unroll
-                            for (int u = 0; u < 16; u += 4)
-                                if (c + u < p.D) __stcg(reinterpret_cast<float4*>(d + u), make_float4(o[u], o[u + 1], o[u + 2], o[u + 3]));
-                        } else {
-                            put16<T>(out + c, o, inv, p.D - c, g.out_vec);
-                        }
-                    }
+                    for (int u = 0; u < 16; ++u) o[u] = 0.0f;
                 }
-                if (r < nrows) {
-                    if (part) {
-                        __stcg(so + (size_t)kRows * p.D + h * kHalf + r, m);
-                        __stcg(so + (size_t)kRows * p.D + kRows + h * kHalf + r, l);
-                    } else if (p.lse) {
-                        p.lse[row * p.Hq + head] = empty ? -INFINITY : (m + log2f(l)) * kLn2;
-                    }
-                }
-                if (part) {
-                    const int c0 = sc.owner(sc.us), c1 = sc.owner(sc.us + sc.c - 1);
-                    __threadfence();
-                    bar_sync(1 + h, kHalf);
-                    if (r == 0) {
-                        const bool last = atomicAdd(p.counters + 2 * c0 + h, 1u) == (unsigned)(c1 - c0);
-                        if (last) p.counters[2 * c0 + h] = 0u;
-                        bars.flag[h] = last;
-                    }
-                    bar_sync(1 + h, kHalf);
-                    if (bars.flag[h]) {
-                        __threadfence();
-                        if (r < nrows) {
-                            const size_t ss = (size_t)kRows * (p.D + 2);
-                            const float* st = p.partials + (size_t)kRows * p.D + h * kHalf + r;
-                            auto slot = [&](int c) { return (size_t)(2 * c + (sc.part(c) >= sc.us ? 0 : 1)) * ss; };
-                            float M = -INFINITY, L = 0.0f;
-                            for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(st + slot(c)));
-                            for (int c = c0; c <= c1; ++c) {
-                                const float pl = __ldcg(st + slot(c) + kRows);
-                                L = fmaf(pl, part_weight(__ldcg(st + slot(c)), pl, M), L);
-                            }
-                            for (int d = 0; d < p.D; d += 16) {
-                                float o[16];
+                if (mine && part) {
 #pragma unroll
-                                for (int u = 0; u < 16; ++u) o[u] = 0.0f;
-                                for (int c = c0; c <= c1; ++c) {
-                                    const float* sp = p.partials + slot(c) + (size_t)(h * kHalf + r) * p.D + d;
-                                    const float pl = __ldcg(st + slot(c) + kRows);
-                                    const float f = part_weight(__ldcg(st + slot(c)), pl, M);
-#pragma unroll
-                                    for (int u = 0; u < 16; u += 4)
-                                        if (d + u < p.D) {
-                                            const float4 v4 = __ldcg(reinterpret_cast<const float4*>(sp + u));
-                                            o[u] = fmaf(v4.x, f, o[u]); o[u + 1] = fmaf(v4.y, f, o[u + 1]);
-                                            o[u + 2] = fmaf(v4.z, f, o[u + 2]); o[u + 3] = fmaf(v4.w, f, o[u + 3]);
-                                        }
-                                }
-                                if (L == 0.0f) {
-#pragma unroll
-                                    for (int u = 0; u < 16; ++u) o[u] = 0.0f;
-                                }
-                                put16<T>(out + d, o, L == 0.0f ? 0.0f : 1.0f / L, p.D - d, g.out_vec);
-                            }
-                            if (p.lse) p.lse[row * p.Hq + head] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
-                        }
-                        bar_sync(1 + h, kHalf);
-                    }
+                    for (int u = 0; u < 16; u += 4)
+                        if (c + u < p.D)
+                            __stcg(reinterpret_cast<float4*>(so + (size_t)at * p.D + c + u), make_float4(o[u], o[u + 1], o[u + 2], o[u + 3]));
+                } else if (mine) {
+                    put16<T>(out + c, o, inv, p.D - c, g.out_vec);
                 }
             }
             tc_before();
-            n0 += k1 - k0;
-            sc.next(p);
+            if (mine && part) {
+                __stcg(so + (size_t)kRows * p.D + at, m);
+                __stcg(so + (size_t)kRows * p.D + kRows + at, l);
+            } else if (mine && p.lse) {
+                p.lse[row * p.Hq + head] = empty ? -INFINITY : (m + log2f(l)) * kLn2;
+            }
+            if (part && nrows > (r & ~31)) {             // this warp has rows
+                // A warp joins its own rows: the last of the unit's blocks to
+                // have written them does.
+                const int c0 = pc->c0, c1 = pc->c1;
+                __threadfence();
+                __syncwarp();
+                int last = 0;
+                if (lane == 0) {
+                    unsigned* cnt = p.counters + 8 * c0 + warp;
+                    last = atomicAdd(cnt, 1u) == (unsigned)(c1 - c0);
+                    if (last) *cnt = 0u;
+                }
+                last = __shfl_sync(0xFFFFFFFFu, last, 0);
+                if (last) {
+                    __threadfence();
+                    if (mine) {
+                        const float* st = p.partials + (size_t)kRows * p.D + at;
+                        auto slot = [&](int c) { return (size_t)(c == c0 ? pc->slot0 : 2 * c) * ss; };
+                        float M = -INFINITY, L = 0.0f;
+#pragma unroll 1
+                        for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(st + slot(c)));
+#pragma unroll 1
+                        for (int c = c0; c <= c1; ++c) {
+                            const float pl = __ldcg(st + slot(c) + kRows);
+                            L = fmaf(pl, part_weight(__ldcg(st + slot(c)), pl, M), L);
+                        }
+                        const float iL = L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll 1
+                        for (int d = 0; d < p.D; d += 16) {
+                            float o[16];
+#pragma unroll
+                            for (int u = 0; u < 16; ++u) o[u] = 0.0f;
+#pragma unroll 1
+                            for (int c = c0; c <= c1; ++c) {
+                                const float* sp = p.partials + slot(c) + (size_t)at * p.D + d;
+                                const float pl = __ldcg(st + slot(c) + kRows);
+                                const float f = part_weight(__ldcg(st + slot(c)), pl, M);
+#pragma unroll
+                                for (int u = 0; u < 16; u += 4)
+                                    if (d + u < p.D) {
+                                        const float4 v4 = __ldcg(reinterpret_cast<const float4*>(sp + u));
+                                        o[u] = fmaf(v4.x, f, o[u]); o[u + 1] = fmaf(v4.y, f, o[u + 1]);
+                                        o[u + 2] = fmaf(v4.z, f, o[u + 2]); o[u + 3] = fmaf(v4.w, f, o[u + 3]);
+                                    }
+                            }
+                            if (L == 0.0f) {
+#pragma unroll
+                                for (int u = 0; u < 16; ++u) o[u] = 0.0f;
+                            }
+                            put16<T>(out + d, o, iL, p.D - d, g.out_vec);
+                        }
+                        if (p.lse) p.lse[row * p.Hq + head] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+                    }
+                }
+            }
+            n0 += pc->k1 - k0;
+            done();
         }
     }
     // ---- every role has ended: tensor memory goes back ------------------------
     tc_before();
     __syncthreads();
     tc_after();
+    __syncwarp();
     if (warp == 8) {
         tm_relinquish();
         tm_dealloc(tm, 512);
@@ -673,8 +766,9 @@ template <class T, int DP, bool MOD> cudaError_t launch_tdm(const AttnParams& p,
         // the warpgroups' shares are drawn from the launch's registers
         cudaFuncAttributes at;
         e = cudaFuncGetAttributes(&at, kern);
-        if (e == cudaSuccess && at.numRegs * kThreads < 256 * kSoftRegs + 128 * kOtherRegs) e = cudaErrorInvalidConfiguration;
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Gm::SMEM);
+        if (e == cudaSuccess && at.numRegs * kThreads < 256 * (kSoftRegs + kOtherRegs)) e = cudaErrorInvalidConfiguration;
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Gm::SMEM);
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }

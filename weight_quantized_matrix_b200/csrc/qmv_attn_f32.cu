@@ -120,8 +120,6 @@ attn_f32_kernel(const __grid_constant__ AttnParams p, int page_shift) {
             at[AHEAD - 1] = place(t + AHEAD);
             issue(t, slot, now);
         };
-#pragma unroll
-        for (int t = 0; t < STAGES - 1; ++t) issue_next(k0 + t, t);
 
         // ---- queries and the rows' keys --------------------------------------
         for (int x = threadIdx.x; x < kRows * CPR; x += NTH) {
@@ -153,11 +151,17 @@ attn_f32_kernel(const __grid_constant__ AttnParams p, int page_shift) {
 #pragma unroll
             for (int u = 0; u < VEC; ++u) o[r][u] = 0.0f;
         }
-        int slot = 0;
-        for (int t = k0; t < k1; ++t) {
-            cp_wait<STAGES - 2>();
-            __syncwarp();
-            issue_next(t + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1);
+        // the first STAGES - 1 rounds only fill the ring
+        int slot = 0, fill = 0;
+#pragma unroll 1
+        for (int t = k0 - (STAGES - 1); t < k1; ++t) {
+            if (t >= k0) {
+                cp_wait<STAGES - 2>();
+                __syncwarp();
+            }
+            issue_next(t + STAGES - 1, fill);                   // the stage read last time
+            fill = fill + 1 == STAGES ? 0 : fill + 1;
+            if (t < k0) continue;
             const unsigned char* kb = mine + slot * Gm::STEP;
             const unsigned char* vb = kb + 16 * ROWB;
             slot = slot + 1 == STAGES ? 0 : slot + 1;
@@ -286,6 +290,7 @@ attn_f32_kernel(const __grid_constant__ AttnParams p, int page_shift) {
             to[0] = v.x * inv; to[1] = v.y * inv; to[2] = v.z * inv; to[3] = v.w * inv;
             if (d == 0 && p.lse) p.lse[row * p.Hq + h] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
         };
+#pragma unroll 1
         for (int x = threadIdx.x; x < nrows * (DP / 4); x += NTH) {
             const int r = x / (DP / 4), d = (x % (DP / 4)) * 4;
             if (d >= p.D) continue;

@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kWarps * 32, FewGeom<DP>::PER_SM) attn_few_ker
                         cp16(d + 16 * ROWB, vl + off);
                     }
                 } else {
-#pragma unroll
+#pragma unroll 2
                     for (int u = 0; u < 16 * CPR / 32; ++u) {
                         const int id = u * 32 + lane, r = id / CPR, c = id % CPR;
                         const int a = __shfl_sync(0xFFFFFFFFu, at, r);
@@ -173,13 +173,19 @@ __global__ void __launch_bounds__(kWarps * 32, FewGeom<DP>::PER_SM) attn_few_ker
             at[AHEAD - 1] = place(t + AHEAD);
             issue(t, slot, now);
         };
-#pragma unroll
-        for (int t = 0; t < STAGES - 1; ++t) issue_next(k0 + t, t);
-        int slot = 0;
-        for (int t = k0; t < k1; ++t) {
-            cp_wait<STAGES - 2>();
-            __syncwarp();
-            issue_next(t + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1);     // the stage read last time
+        // The first STAGES - 1 rounds only fill the ring.  (One copy of the code for
+        // them too: unrolled fills made the kernel 160 KB, and a short call waited
+        // for its instructions.)
+        int slot = 0, fill = 0;
+#pragma unroll 1
+        for (int t = k0 - (STAGES - 1); t < k1; ++t) {
+            if (t >= k0) {
+                cp_wait<STAGES - 2>();
+                __syncwarp();
+            }
+            issue_next(t + STAGES - 1, fill);                   // the stage read last time
+            fill = fill + 1 == STAGES ? 0 : fill + 1;
+            if (t < k0) continue;
             const uint32_t kb = mine_a + slot * Gm::STEP, vb = kb + 16 * ROWB;
             slot = slot + 1 == STAGES ? 0 : slot + 1;
             const int j0 = t * kTile + warp * 16;
@@ -253,6 +259,7 @@ __global__ void __launch_bounds__(kWarps * 32, FewGeom<DP>::PER_SM) attn_few_ker
             // finite model makes one) adds key by key.
             bool odd = false;
             if (!full) {
+#pragma unroll 1
                 for (int u = 0; u < 16 * CPR / 32; ++u) {
                     const uint4 w = *reinterpret_cast<const uint4*>(mine + (vb - mine_a) + (u * 32 + lane) * 16);
                     odd |= odd_word<T>(w.x) || odd_word<T>(w.y) || odd_word<T>(w.z) || odd_word<T>(w.w);
@@ -271,11 +278,12 @@ __global__ void __launch_bounds__(kWarps * 32, FewGeom<DP>::PER_SM) attn_few_ker
                     mma<T>(o[n + 1], pf, f[2], f[3]);
                 }
             } else {
-#pragma unroll
+#pragma unroll 1
                 for (int k = 0; k < 16; ++k) {
                     const int j = j0 + k, src = (lane & ~3) | ((k & 7) >> 1);
-                    const float p0 = __shfl_sync(0xFFFFFFFFu, sa[k >> 3][k & 1], src);
-                    const float p1 = __shfl_sync(0xFFFFFFFFu, sa[k >> 3][2 + (k & 1)], src);
+                    const float c0 = k & 8 ? (k & 1 ? sa[1][1] : sa[1][0]) : (k & 1 ? sa[0][1] : sa[0][0]);
+                    const float c1 = k & 8 ? (k & 1 ? sa[1][3] : sa[1][2]) : (k & 1 ? sa[0][3] : sa[0][2]);
+                    const float p0 = __shfl_sync(0xFFFFFFFFu, c0, src), p1 = __shfl_sync(0xFFFFFFFFu, c1, src);
                     const bool v0 = j >= lo[0] && j < hi[0], v1 = j >= lo[1] && j < hi[1];
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
@@ -314,6 +322,7 @@ __global__ void __launch_bounds__(kWarps * 32, FewGeom<DP>::PER_SM) attn_few_ker
             st_elem(to, v.x * inv); st_elem(to + 1, v.y * inv); st_elem(to + 2, v.z * inv); st_elem(to + 3, v.w * inv);
             if (d == 0 && p.lse) p.lse[row * p.Hq + h] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
         };
+#pragma unroll 1
         for (int x = threadIdx.x; x < nrows * (DP / 4); x += kWarps * 32) {
             const int r = x / (DP / 4), d = (x % (DP / 4)) * 4;
             if (d >= p.D) continue;

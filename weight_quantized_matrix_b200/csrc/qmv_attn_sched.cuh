@@ -64,54 +64,50 @@ constexpr int kAlignTiles = 64;         // parts up to this many tiles end with 
 
 struct SchedSmem {
     long long warp_sum[32];
-    long long seq_at;       // tiles before the sequence in which the block's part begins
+    long long seq_at;       // chunks before the sequence in which the block's part begins
     int seq;                // that sequence
-    long long per_head;     // its tiles per kv head
+    int per_head;           // its chunks per kv head
 };
 
-// a / b; 32-bit when both fit (a 64-bit division is a call of a hundred instructions).
-__device__ __forceinline__ long long tile_div(long long a, long long b) {
-    if (((a | b) >> 31) == 0) return (long long)((unsigned)a / (unsigned)b);
-    return a / b;
-}
-
-// One block's walk over its part.
+// One block's walk over its part.  Work is counted in chunks of Q key tiles of a
+// unit (its last chunk may be shorter): Q = 1 unless parts are to end with their
+// units, or there are more tiles than an int counts.
 template <int ROWS, int TK> struct Sched {
-    long long W, w0, w1;    // all tiles, this block's part
-    long long q, rem;       // W = nblk q + rem: the first rem blocks take q + 1 tiles
-    long long us;           // first tile of the current unit
-    int nblk, b, h, i, c;   // blocks with a part; current unit and its cost in tiles
+    int W, w0, w1;          // all chunks, this block's part
+    int q, rem;             // W = nblk q + rem: the first rem blocks take q + 1 chunks
+    int us;                 // first chunk of the current unit
+    int nblk, b, h, i, c;   // blocks with a part; current unit and its chunks
     int first, nt;          // its first key tile and number of key tiles
-    int Q;                  // costs are rounded up to multiples of Q
+    int Q;
     SeqInfo s;
     bool split, live;
 
-    __device__ __forceinline__ int padded(int tiles) const {
-        return tiles <= Q ? Q : Q == 1 ? tiles : (tiles + Q - 1) / Q * Q;
+    __device__ __forceinline__ int chunks(int tiles) const {
+        return tiles <= Q ? 1 : Q == 1 ? tiles : (tiles - 1) / Q + 1;
     }
-    __device__ __forceinline__ long long part(int blk) const { return blk * q + min((long long)blk, rem); }
-    __device__ __forceinline__ int owner(long long w) const {
-        const long long big = rem * (q + 1);
-        return (int)(w < big ? tile_div(w, q + 1) : rem + tile_div(w - big, q));
+    __device__ __forceinline__ int part(int blk) const { return blk * q + min(blk, rem); }
+    __device__ __forceinline__ int owner(int w) const {
+        const int big = rem * (q + 1);
+        return w < big ? w / (q + 1) : rem + (w - big) / q;
     }
-
     __device__ __forceinline__ void load_unit(const AttnParams& p) {
         nt = unit_tiles<ROWS, TK>(p, s, i, first);
-        c = padded(nt);
+        c = chunks(nt);
     }
     __device__ __forceinline__ void next(const AttnParams& p) {
         us += c;
+        if (us >= w1) { live = false; return; }
         if (++i * ROWS >= s.n * p.G) {
             i = 0;
             if (++h == p.Hkv) {
                 h = 0;
+#pragma unroll 1
                 do {
                     if (++b >= p.n_seqs) { live = false; return; }
                     s = seq_info(p, b);
                 } while (s.n == 0);
             }
         }
-        if (us >= w1) { live = false; return; }
         load_unit(p);
     }
     // Every thread of the block calls this (NT threads, LPS lanes a sequence).
@@ -121,16 +117,17 @@ template <int ROWS, int TK> struct Sched {
         int only = -1;          // tiles of the thread's sequence where it has one row tile and there is one round
         const int rounds = (p.n_seqs + SEQS - 1) / SEQS;
         auto cost = [&](int bb) {
-            long long v = 0;
-            if (LPS == 1 && only >= 0) return (long long)padded(only);
+            int v = 0;
+            if (LPS == 1 && only >= 0) return chunks(only);
             if (bb < p.n_seqs) {
                 const SeqInfo si = seq_info(p, bb);
                 const int nq = (si.n * p.G + ROWS - 1) / ROWS;
                 int f;
+#pragma unroll 1
                 for (int k = sub; k < nq; k += LPS) {
                     const int tiles = unit_tiles<ROWS, TK>(p, si, k, f);
                     if (nq == 1 && rounds == 1) only = tiles;
-                    v += padded(tiles);
+                    v += chunks(tiles);
                 }
             }
 #pragma unroll
@@ -138,8 +135,8 @@ template <int ROWS, int TK> struct Sched {
             return v;
         };
         // inclusive scan over the block (the value counts once a sequence)
-        auto scan = [&](long long v, long long& total) {
-            v = sub == 0 ? v * p.Hkv : 0;
+        auto scan = [&](int c1, long long& total) {
+            long long v = sub == 0 ? (long long)c1 * p.Hkv : 0;
 #pragma unroll
             for (int w = 1; w < 32; w <<= 1) {
                 const long long u = __shfl_up_sync(0xFFFFFFFFu, v, w);
@@ -160,45 +157,55 @@ template <int ROWS, int TK> struct Sched {
         };
         split = p.partials != nullptr;
         live = false;
-        long long v = 0, incl = 0;
-        auto count = [&]() {
-            W = 0;
+        Q = 1;
+        int v = 0, pass = 0;    // 0: count tiles, 1: parts end with their units, 2: they do not
+        long long incl = 0, all;
+#pragma unroll 1
+        for (;;) {
+            all = 0;
+#pragma unroll 1
             for (int r = 0; r < rounds; ++r) {
                 v = cost(r * SEQS + tid / LPS);
                 long long total;
                 incl = scan(v, total);
-                W += total;
+                all += total;
             }
-        };
-        Q = 1;
-        count();
-        if (W == 0) return;
-        nblk = (int)min((long long)gridDim.x, max(1LL, tile_div(W, min_tiles)));
-        const long long each = tile_div(W + gridDim.x - 1, gridDim.x);
-        if (split && each <= kAlignTiles) {
-            const long long all = W;
-            Q = max((int)each, min_tiles);
-            count();
-            if (tile_div(W, Q) <= gridDim.x) {
-                nblk = (int)tile_div(W, Q);
-            } else {
+            if (pass == 0) {
+                if (all == 0) return;
+                if (all >> 30) {
+                    Q = (int)(all >> 29) + 1;
+                    pass = 2;
+                    continue;
+                }
+                const int each = (int)(((unsigned)all + gridDim.x - 1) / gridDim.x);
+                if (split && each <= kAlignTiles) {
+                    Q = max(each, min_tiles);
+                    pass = 1;
+                    continue;
+                }
+            } else if (pass == 1 && all > (long long)gridDim.x) {
                 Q = 1;
-                if (rounds > 1) W = all; else count();
+                pass = 2;
+                continue;
             }
+            break;
         }
+        W = (int)all;
+        nblk = pass == 1 ? W : min((int)gridDim.x, max(1, Q == 1 ? W / min_tiles : W));
         if ((int)blockIdx.x >= nblk) return;
-        q = tile_div(W, nblk);
+        q = W / nblk;
         rem = W - q * nblk;
         w0 = part(blockIdx.x);
         w1 = part(blockIdx.x + 1);
         long long base = 0;
+#pragma unroll 1
         for (int r = 0; r < rounds; ++r) {
-            long long total = W;
+            long long total = all;
             if (rounds > 1) {
                 v = cost(r * SEQS + tid / LPS);
                 incl = scan(v, total);
             }
-            const long long end = base + incl, beg = end - v * p.Hkv;
+            const long long end = base + incl, beg = end - (long long)v * p.Hkv;
             if (sub == 0 && beg <= w0 && w0 < end) {
                 sm.seq = r * SEQS + tid / LPS;
                 sm.seq_at = beg;
@@ -210,16 +217,17 @@ template <int ROWS, int TK> struct Sched {
         __syncthreads();
         b = sm.seq;
         s = seq_info(p, b);
-        long long off = w0 - sm.seq_at;
-        h = (int)tile_div(off, sm.per_head);
+        int off = w0 - (int)sm.seq_at;
+        h = off / sm.per_head;
         off -= h * sm.per_head;
-        i = 0;
-        load_unit(p);
-        while (off >= c) {
+        i = -1;
+        c = 0;
+#pragma unroll 1
+        do {
             off -= c;
             ++i;
             load_unit(p);
-        }
+        } while (off >= c);
         us = w0 - off;
         live = true;
         if (!split && off > 0) next(p);     // the unit belongs to the block before
@@ -227,8 +235,8 @@ template <int ROWS, int TK> struct Sched {
     // Key tiles [k0, k1) of the current unit that are this block's.
     __device__ __forceinline__ void piece(int& k0, int& k1) const {
         if (split) {
-            k0 = first + (int)(max(w0, us) - us);
-            k1 = first + min((int)(min(w1, us + c) - us), nt);
+            k0 = first + (max(w0, us) - us) * Q;
+            k1 = first + min((min(w1, us + c) - us) * Q, nt);
         } else {
             k0 = first;
             k1 = first + nt;
@@ -287,6 +295,7 @@ __device__ __forceinline__ void attn_join(const AttnParams& p, const Sched<ROWS,
     for (int i = tid; i < np; i += NT) s_slot[i] = (c0 + i) * 2 + (sc.part(c0 + i) >= sc.us ? 0 : 1);
     __syncthreads();
     const size_t ss = (size_t)ROWS * (p.D + 2);
+#pragma unroll 1
     for (int x = tid; x < nrows * np; x += NT) {
         const int r = x / np, i = x - r * np;
         const float* so = p.partials + s_slot[i] * ss + ROWS * p.D;
@@ -310,6 +319,7 @@ __device__ __forceinline__ void attn_join(const AttnParams& p, const Sched<ROWS,
     }
     __syncthreads();
     const int vecs = p.D / 4;
+#pragma unroll 1
     for (int x = tid; x < nrows * vecs; x += NT) {
         const int r = x / vecs, d = (x - r * vecs) * 4;
         const float* so = p.partials + r * p.D + d;
