@@ -1,6 +1,7 @@
 // qmv_attn.cuh -- device pieces of the paged attention kernels.
 #pragma once
 
+#include "qmv_attn_mma.cuh"
 #include "qmv_paged.cuh"
 
 namespace qmv {
@@ -47,6 +48,48 @@ template <bool EXACT> struct ScoreMod {
             }
         }
         return fmaf(slope_log2, (float)away, s);
+    }
+    // N scores of consecutive keys, the first `away` from the row's position.
+    // Where every |s / c| of the warp is at most 0.7 (scores seldom come near their
+    // cap) tanh is its odd polynomial, fitted to 2^-26 there: no exponential and
+    // no division, which are the scarce units in a softmax.
+    template <int N> __device__ __forceinline__ void apply_all(float (&x)[N], float slope_log2, int away) const {
+        const float2 pre2 = make_float2(pre, pre);
+        if (cap) {
+            float big = 0.0f;
+#pragma unroll
+            for (int c = 0; c < N; ++c) big = fmaxf(big, fabsf(x[c]));
+            const float half = pre * (0.5f * kLn2);             // pre holds 2 log2 e / c
+            if (__all_sync(0xFFFFFFFFu, big * half <= 0.7f)) {
+                const float2 h2 = make_float2(half, half), post2 = make_float2(post, post);
+#pragma unroll
+                for (int c = 0; c < N; c += 2) {
+                    const float2 t = mul2(make_float2(x[c], x[c + 1]), h2), u = mul2(t, t);
+                    float2 r = fma2(make_float2(-0.00515510421f, -0.00515510421f), u, make_float2(0.0201116465f, 0.0201116465f));
+                    r = fma2(r, u, make_float2(-0.0535669848f, -0.0535669848f));
+                    r = fma2(r, u, make_float2(0.133292437f, 0.133292437f));
+                    r = fma2(r, u, make_float2(-0.333331972f, -0.333331972f));
+                    const float2 w = mul2(t, post2), v = fma2(mul2(w, u), r, w);
+                    x[c] = v.x;
+                    x[c + 1] = v.y;
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < N; ++c) x[c] = apply(x[c], 0.0f, 0);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < N; c += 2) {
+                const float2 v = mul2(make_float2(x[c], x[c + 1]), pre2);
+                x[c] = v.x;
+                x[c + 1] = v.y;
+            }
+        }
+        if (slope_log2 != 0.0f) {
+            const float a0 = (float)away;
+#pragma unroll
+            for (int c = 0; c < N; ++c) x[c] = fmaf(slope_log2, a0 + (float)c, x[c]);
+        }
     }
 };
 

@@ -67,7 +67,6 @@ struct Piece {
     int k0, k1;              // key tiles
     int ulo, uhi;            // keys that any row sees
     int a[2], e[2];          // key tiles of each half
-    int plo[2], phi[2];      // keys that every row of a half sees
     int shared;              // other blocks have parts of the unit
     int slot;                // this block's partial result
     int c0, c1, slot0;       // first and last block of the unit; the first one's partial result
@@ -80,7 +79,7 @@ struct Bars {
     uint64_t pc_full[kPieces], pc_empty[kPieces];
     uint32_t tmem;
     volatile int abort;
-    int skip[2][2];          // the second product was done by the softmax warps
+    int turn[4];             // taken while a warp of the scheduler's pair has its exponentials
 };
 
 struct ChunkArgs {
@@ -122,44 +121,60 @@ __device__ __forceinline__ bool warp_wait_all(Waiter& w, uint32_t bar, uint32_t 
     return w.ok;
 }
 
-// O += P V of one tile for this thread's row, key by key: keys [lo, hi) of the
-// tile are the ones the row sees.
-template <class T, int DP>
-__device__ __forceinline__ void add_by_hand(uint32_t to, uint32_t tp, const unsigned char* v, bool acc, int lo, int hi) {
+// The two softmax warps of a scheduler (one of each half) take turns at their
+// exponentials.  At once they take twice as long each, fall into step and leave
+// the exponentials' unit idle for the rest of the step; in turns one warp's
+// exponentials run beside the other's loads, maxima and waits.  Only the speed
+// depends on it: after a while a warp goes on without its turn.
+__device__ __forceinline__ void take_turn(int* turn) {
+    if ((threadIdx.x & 31) == 0) {
+        for (int i = 0; i < 200 && atomicExch(turn, 1) != 0; ++i) {}
+    }
+    __syncwarp();
+}
+__device__ __forceinline__ void give_turn(int* turn) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) *(volatile int*)turn = 0;
+}
+
+// One row over keys [k0, k1) of its sequence, by a warp (lane = dims lane, lane +
+// 32, ..), reading only the keys the row sees: for rows whose sums came out
+// infinite or NaN.  There, and only there, a value that some rows see and others
+// do not may have reached the others through 0 * v.
+template <class T, int DP, bool MOD>
+__device__ __forceinline__ void exact_row(const AttnParams& p, const ScoreMod<false>& mod, int b, int hk, const T* q, int pos,
+                                          int k0, int k1, float slope, float (&o)[DP / 32], float& m, float& l) {
+    const int lane = threadIdx.x & 31;
+    float qv[DP / 32];
+#pragma unroll
+    for (int i = 0; i < DP / 32; ++i) {
+        const int d = lane + 32 * i;
+        qv[i] = d < p.D ? ld_elem(q + d) : 0.0f;
+        o[i] = 0.0f;
+    }
+    m = -INFINITY;
+    l = 0.0f;
 #pragma unroll 1
-    for (int c = 0; c < DP; c += 16) {
-        float o[16];
+    for (int j = k0; j < k1; ++j) {
+        const long long at = key_place(p, b, hk, j);
+        float s = 0.0f;
 #pragma unroll
-        for (int u = 0; u < 16; ++u) o[u] = 0.0f;
-        __syncwarp();
-        if (acc) { tm_ld16(to + c, o); tm_wait_ld(); }
-#pragma unroll 1
-        for (int k = 0; k < kTile; ++k) {
-            uint32_t w2;
-            __syncwarp();
-            tm_ld1(tp + k / 2, w2);
-            tm_wait_ld();
-            const float2 pw = unpack2<T>(w2);
-            if (k >= lo && k < hi) {
-                const float pe = k & 1 ? pw.y : pw.x;
-#pragma unroll
-                for (int u = 0; u < 16; u += 8) {
-                    const int ch = (c + u) / 8;
-                    const uint4 vv = *reinterpret_cast<const uint4*>(v + (ch / 8) * (kTile * 128) + k * 128 +
-                                                                     (((ch & 7) ^ (k & 7)) << 4));
-                    const uint32_t vw[4] = {vv.x, vv.y, vv.z, vv.w};
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const float2 f2 = unpack2<T>(vw[t]);
-                        o[u + 2 * t] = fmaf(pe, f2.x, o[u + 2 * t]);
-                        o[u + 2 * t + 1] = fmaf(pe, f2.y, o[u + 2 * t + 1]);
-                    }
-                }
-            }
+        for (int i = 0; i < DP / 32; ++i) {
+            const int d = lane + 32 * i;
+            if (at >= 0 && d < p.D) s = fmaf(qv[i], ld_elem(static_cast<const T*>(p.k) + at + d), s);
         }
-        __syncwarp();
-        tm_st16(to + c, reinterpret_cast<uint32_t*>(o));
-        tm_wait_st();
+#pragma unroll
+        for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, w);
+        s = at < 0 ? NAN : MOD ? mod.apply(s, slope, j - pos) : s * p.scale * kLog2e;
+        const float mn = fmaxf(m, s), base = mn == -INFINITY ? 0.0f : mn, f = ex2(m - base), w = ex2(s - base);
+        l = fmaf(l, f, w);
+        m = mn;
+#pragma unroll
+        for (int i = 0; i < DP / 32; ++i) {
+            const int d = lane + 32 * i;
+            o[i] = at >= 0 && d < p.D ? fmaf(w, ld_elem(static_cast<const T*>(p.v) + at + d), o[i] * f) : o[i] * f;
+            if (at < 0) o[i] = NAN;
+        }
     }
 }
 
@@ -186,11 +201,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
             for (int u = 0; u < 2; ++u) {
                 mbar_init1(&bars.p_full[i][u], 4);
                 mbar_init1(&bars.pv_done[i][u], 1);
-                bars.skip[i][u] = 0;
             }
             mbar_init1(&bars.drain[i], 1);
         }
         for (int i = 0; i < kPieces; ++i) { mbar_init1(&bars.pc_full[i], 1); mbar_init1(&bars.pc_empty[i], kReaders); }
+        for (int i = 0; i < 4; ++i) bars.turn[i] = 0;
         bars.abort = 0;
         fence_mbar_init();
     }
@@ -245,18 +260,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
 #pragma unroll 1
                         for (int h = 0; h < 2; ++h) {
                             const int r0 = rbase + h * kHalf, r1 = min(r0 + kHalf, rows) - 1;
-                            int a = k0, e = k0, plo = 0, phi = 0;
+                            int a = k0, e = k0;
                             if (r0 <= r1) {
                                 int lo, hi;
-                                visible_keys(p, sc.s.len - sc.s.n + r0 / p.G, sc.s.len, lo, phi);
-                                visible_keys(p, sc.s.len - sc.s.n + r1 / p.G, sc.s.len, plo, hi);
+                                rows_keys(p, sc.s, r0, r1, lo, hi);
                                 if (lo < hi) {
                                     a = max(k0, lo / kTile);
                                     e = min(k1, (hi + kTile - 1) / kTile);
                                     if (a >= e) a = e = k0;
                                 }
                             }
-                            pc.a[h] = a; pc.e[h] = e; pc.plo[h] = plo; pc.phi[h] = phi;
+                            pc.a[h] = a; pc.e[h] = e;
                         }
                         pc.shared = sc.shared();
                         pc.slot = 2 * blockIdx.x + (sc.w0 >= sc.us ? 0 : 1);
@@ -272,8 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
             }
         } else if (warp < 10) {
             // ------------------------------------------------ the products ----
-            // One warp a half.  The whole warp walks through this with the same
-            // values and one lane issues.  These warps share their schedulers with
+            // One warp a half, of which one lane walks the steps.  These warps share their schedulers with
             // the softmax and wait for every instruction of their own: slots,
             // phases and descriptors are counted up, not computed.
             const int h = warp - 8;
@@ -300,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                     // the softmax holds the S before in registers
                     if (sn > 0) wait(se_a, (uint32_t)(sn - 1) & 1u);
                     tc_after();
-                    if (one && wait.ok) {
+                    if (wait.ok) {
                         const uint32_t b = (ring_d + ks * (Gm::SLOT / 16)) | LBO_K;
 #pragma unroll
                         for (int k = 0; k < DP / 16; ++k) {
@@ -311,14 +324,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                     }
                     ++sn;
                 }
-                if (one && wait.ok) commit(empty_a + ks * 8);
+                if (wait.ok) commit(empty_a + ks * 8);
                 ks += 2;
                 if (ks == SLOTS) { ks = 0; kph ^= 1u; }
             };
 #pragma unroll 1
             while (const Piece* pc = take(wait)) {
                 const int k0 = pc->k0, k1 = pc->k1, a = pc->a[h], e = pc->e[h];
-                if (k0 < k1) {
+                if (one && k0 < k1) {
                     wait(s_addr(&bars.q_full), qph);
                     qph ^= 1u;
                     // first products k0 .. k1 - 1, each one step ahead of its second
@@ -326,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                     for (int j = k0 - 1; j < k1 && wait.ok; ++j) {
                         if (j + 1 < k1) {
                             qk(a <= j + 1 && j + 1 < e);
-                            if (j + 2 == k1 && one) commit(qe_a);
+                            if (j + 2 == k1) commit(qe_a);
                         }
                         if (j < k0) continue;
                         wait(full_a + vs * 8, vph);
@@ -334,19 +347,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                             const int u = pn & 1;
                             wait(pf_a + u * 8, (uint32_t)(pn >> 1) & 1u);
                             tc_after();
-                            if (one && wait.ok) {
-                                if (!*(volatile int*)&bars.skip[h][u]) {
-                                    const uint32_t v = (ring_d + vs * (Gm::SLOT / 16)) | LBO_V, w = tp + u * 32;
-                                    mma_ts(to, w, v, HI, ID_O, j > a);
+                            if (wait.ok) {
+                                const uint32_t v = (ring_d + vs * (Gm::SLOT / 16)) | LBO_V, w = tp + u * 32;
+                                mma_ts(to, w, v, HI, ID_O, j > a);
 #pragma unroll
-                                    for (int k = 1; k < kTile / 16; ++k)
-                                        mma_ts(to, w + k * 8, v + k * (16 * 128 / 16), HI, ID_O, true);
-                                }
+                                for (int k = 1; k < kTile / 16; ++k)
+                                    mma_ts(to, w + k * 8, v + k * (16 * 128 / 16), HI, ID_O, true);
                                 commit(pv_a + u * 8);
                             }
                             ++pn;
                         }
-                        if (one && wait.ok) commit(empty_a + vs * 8);
+                        if (wait.ok) commit(empty_a + vs * 8);
                         vs += 2;
                         if (vs > SLOTS) { vs = 1; vph ^= 1u; }
                     }
@@ -508,10 +519,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         const float scale2 = p.scale * kLog2e;
         Waiter wait{&bars, p.fault, 1u, true};
         int ns = 0;                                      // steps of this half so far
-        int n0 = 0;                                      // tiles of all pieces before this one
 #pragma unroll 1
         while (const Piece* pc = take(wait)) {
-            const int k0 = pc->k0, a = pc->a[h], e = pc->e[h];
+            const int a = pc->a[h], e = pc->e[h];
             const int rbase = pc->rbase + h * kHalf, nrows = min(kHalf, pc->n * p.G - rbase);
             int lo = 0, hi = 0, pos = 0, ti = 0, head = 0;
             float slope = 0.0f;
@@ -523,8 +533,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                 visible_keys(p, pos, pc->len, lo, hi);
                 if (MOD && p.slopes) slope = __ldg(p.slopes + head) * kLog2e;
             }
-            // keys that every row of the half sees
-            const int part_lo = pc->plo[h], part_hi = pc->phi[h];
             float m = -INFINITY, l = 0.0f;
 #pragma unroll 1
             for (int j = a; j < e && wait.ok; ++j, ++ns) {
@@ -542,10 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                 tc_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive1(&bars.s_empty[h]);      // the next S may be written
-                if constexpr (MOD) {
-#pragma unroll
-                    for (int c = 0; c < kTile; ++c) x[c] = mod.apply(x[c], slope, j0 + c - pos);
-                }
+                if constexpr (MOD) mod.template apply_all<kTile>(x, slope, j0 - pos);
                 if (!full) {
 #pragma unroll
                     for (int c = 0; c < kTile; ++c)
@@ -586,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                 }
                 // this P was last read by the second product two steps ago
                 if (ns >= 2 && !warp_wait_all(wait, s_addr(&bars.pv_done[h][u2]), (uint32_t)((ns >> 1) - 1) & 1u)) break;
-                __syncwarp();
+                take_turn(&bars.turn[warp & 3]);
                 tc_after();
                 const float base = m == -INFINITY ? 0.0f : m;
                 const float2 nb = make_float2(-base, -base), sc2 = make_float2(MOD ? 1.0f : scale2, MOD ? 1.0f : scale2);
@@ -604,32 +609,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                     }
                     tm_st16(tp + c / 2, pk);
                 }
+                give_turn(&bars.turn[warp & 3]);
                 l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
                 tm_wait_st();
-                // Where some rows see a key and others do not, an infinite or NaN
-                // value must not reach the others through 0 * v: the half's warps
-                // (each finds out for itself) then add such a tile, which no
-                // finite model makes, key by key.
-                if (j0 < part_lo || j0 + kTile > part_hi) {
-                    const int x2 = 2 * (n0 + j - k0) + 1;
-                    if (!warp_wait_all(wait, s_addr(&bars.kv_full[x2 % SLOTS]), (uint32_t)(x2 / SLOTS) & 1u)) break;
-                    const unsigned char* v = smem + Gm::RING + (x2 % SLOTS) * Gm::SLOT;
-                    bool odd = false;
-#pragma unroll 4
-                    for (int u = lane; u < Gm::SLOT / 16; u += 32) {
-                        const uint4 q4 = reinterpret_cast<const uint4*>(v)[u];
-                        odd |= odd_word<T>(q4.x) || odd_word<T>(q4.y) || odd_word<T>(q4.z) || odd_word<T>(q4.w);
-                    }
-                    odd = __any_sync(0xFFFFFFFFu, odd);
-                    if (odd) {
-                        if (j > a && !warp_wait_all(wait, s_addr(&bars.pv_done[h][u2 ^ 1]), (uint32_t)((ns - 1) >> 1) & 1u)) break;
-                        tc_after();
-                        add_by_hand<T, DP>(to, tp, v, j > a, lo - j0, hi - j0);
-                    }
-                    if (r == 0) bars.skip[h][u2] = odd;
-                } else if (r == 0) {
-                    bars.skip[h][u2] = 0;
-                }
                 tc_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive1(&bars.p_full[h][u2]);
@@ -646,11 +628,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
             const size_t ss = (size_t)kRows * (p.D + 2);
             const int at = h * kHalf + r;                // row of the unit
             float* so = p.partials + pc->slot * ss;
+            bool odd = false;                            // a sum that is not finite
 #pragma unroll 1
             for (int c = 0; c < p.D; c += 16) {
                 float o[16];
                 __syncwarp();
                 if (any) { tm_ld16(to + c, o); tm_wait_ld(); }
+#pragma unroll
+                for (int u = 0; u < 16; ++u) odd |= !(fabsf(o[u]) < INFINITY);
                 if (empty) {
 #pragma unroll
                     for (int u = 0; u < 16; ++u) o[u] = 0.0f;
@@ -670,6 +655,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                 __stcg(so + (size_t)kRows * p.D + kRows + at, l);
             } else if (mine && p.lse) {
                 p.lse[row * p.Hq + head] = empty ? -INFINITY : (m + log2f(l)) * kLn2;
+            }
+            unsigned again = __ballot_sync(0xFFFFFFFFu, mine && any && odd && !empty);
+#pragma unroll 1
+            while (again) {
+                const int src = __ffs(again) - 1;
+                again &= again - 1;
+                __syncwarp();
+                auto of = [&](int v) { return __shfl_sync(0xFFFFFFFFu, v, src); };
+                const int sti = of(ti), shead = of(head), spos = of(pos), slo = max(of(lo), a * kTile), shi = min(of(hi), e * kTile);
+                const float sslope = __shfl_sync(0xFFFFFFFFu, slope, src);
+                float o[DP / 32], sm2, sl;
+                exact_row<T, DP, MOD>(p, mod, pc->b, pc->h, static_cast<const T*>(p.q) + (long long)(pc->t0 + sti) * p.q_ts + (long long)shead * p.q_hs,
+                                      spos, slo, shi, sslope, o, sm2, sl);
+                const int sat = h * kHalf + (r & ~31) + src;
+                const long long srow = pc->t0 + sti;
+#pragma unroll
+                for (int i = 0; i < DP / 32; ++i) {
+                    const int d = lane + 32 * i;
+                    if (d >= p.D) continue;
+                    if (part) __stcg(so + (size_t)sat * p.D + d, sl == 0.0f ? 0.0f : o[i]);
+                    else st_elem(static_cast<T*>(p.out) + srow * p.o_ts + (long long)shead * p.o_hs + d, sl == 0.0f ? 0.0f : o[i] / sl);
+                }
+                if (lane == 0 && part) {
+                    __stcg(so + (size_t)kRows * p.D + sat, sm2);
+                    __stcg(so + (size_t)kRows * p.D + kRows + sat, sl);
+                } else if (lane == 0 && p.lse) {
+                    p.lse[srow * p.Hq + shead] = sl == 0.0f ? -INFINITY : (sm2 + log2f(sl)) * kLn2;
+                }
             }
             if (part && nrows > (r & ~31)) {             // this warp has rows
                 // A warp joins its own rows: the last of the unit's blocks to
@@ -726,7 +739,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                     }
                 }
             }
-            n0 += pc->k1 - k0;
             done();
         }
     }
