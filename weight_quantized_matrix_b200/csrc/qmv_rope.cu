@@ -10,10 +10,10 @@
 // once to the element type.
 //
 // Memory-bound: every element is read once and written once.  A block takes
-// `tpb` tokens (as many as give its 256 threads two vectors each); its threads
-// first load their vectors, then share out the tokens' cosines and sines
-// through shared memory (one evaluation per token and pair, for all heads),
-// then rotate and store.  A work item is the pair of vectors a rotation mixes:
+// `tpb` tokens (as many as give its 256 threads two items each); its threads
+// first load their vectors, then look the tokens up and share out their cosines
+// and sines through shared memory (one evaluation per token and pair, for all
+// heads), then rotate and store.  A work item is the pair of vectors a rotation mixes:
 // dims (i, i + rot/2) of the half layout, or 2 consecutive vectors of the
 // interleaved one and of the parts that are copied (dims >= rot, V).
 #include "qmv_paged.cuh"
@@ -24,6 +24,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 32;      // tokens of a block
+constexpr int kItems = 2;           // items a thread holds at once
 
 template <int BYTES> struct VecOf;
 template <> struct VecOf<16> { using type = uint4; };
@@ -46,13 +47,22 @@ template <class T, int E> union Vec {
     __device__ Vec() {}
 };
 
-// One work item: where its two vectors come from and go to, and how they turn.
-struct Item {
-    const void* src[2];
-    void* dst[2];
-    int cs;                         // index of the first cos / sin, -1: copied
-    int n;                          // vectors (a head's last pair may hold one)
-    int n_turn;                     // interleaved: how many of them turn
+// n / d for n < 2^31: by the reciprocal where that is exact (n d < 2^32), else plainly.
+struct Div {
+    unsigned d, mul;                // mul 0: plain
+    __device__ __forceinline__ int operator()(int n) const {
+        return mul ? (int)__umulhi((unsigned)n, mul) : n / (int)d;
+    }
+};
+Div make_div(long long d, long long max_n) {
+    Div v{(unsigned)d, 0u};
+    if (d > 1 && max_n * d < (1LL << 32)) v.mul = (unsigned)((1ULL << 32) / d + 1);
+    return v;
+}
+
+struct RopeShape {
+    int tpb, heads, ipr_rot, ipr_copy, per_tok;     // heads that turn; items of a turning and of a copied head, of a token
+    Div by_tok, by_rot, by_copy;
 };
 
 struct Smem {
@@ -62,59 +72,45 @@ struct Smem {
     int live[kMaxTokens];           // 0: row outside every sequence
 };
 
-template <class T, int E>
-__device__ __forceinline__ bool find_item(const RopeParams& p, const Smem& s, long long t0, int ntok, int i,
-                                          int ipr_rot, int ipr_copy, Item& it) {
-    // first the heads that turn (the leading p.skip are left alone), then V
-    const int heads = p.H - p.n_kv - p.skip;
-    const int per_tok = heads * ipr_rot + p.n_kv * ipr_copy;
-    if (i >= ntok * per_tok) return false;
-    const int lt = i / per_tok;
-    int r = i - lt * per_tok;
-    int h, j;
-    const bool turns = r < heads * ipr_rot;
-    if (turns) {
-        h = r / ipr_rot;
-        j = r - h * ipr_rot;
-        h += p.skip;
+// One work item: two vectors of a head, at dims a and b.
+struct Item {
+    int lt, h, a, b;                // token of the block, head
+    int cs;                         // index of the first cos / sin of a token, -1: copied
+    int n;                          // vectors (a head's last pair may hold one)
+    int n_turn;                     // interleaved: how many of them turn
+};
+
+template <int E> __device__ __forceinline__ Item item_of(const RopeParams& p, const RopeShape& g, int i) {
+    Item it;
+    it.lt = g.by_tok(i);
+    int r = i - it.lt * g.per_tok, j;
+    const bool turns = r < g.heads * g.ipr_rot;
+    if (turns) {                    // the leading p.skip heads are left alone
+        it.h = g.by_rot(r);
+        j = r - it.h * g.ipr_rot;
+        it.h += p.skip;
     } else {
-        r -= heads * ipr_rot;
-        h = r / ipr_copy;
-        j = r - h * ipr_copy;
-        h += p.H - p.n_kv;
+        r -= g.heads * g.ipr_rot;
+        it.h = g.by_copy(r);
+        j = r - it.h * g.ipr_copy;
+        it.h += p.H - p.n_kv;
     }
-    if (!s.live[lt]) return false;
-    T* d;
-    if (h < p.n_dst) {
-        d = static_cast<T*>(p.dst) + (t0 + lt) * p.dst_ts + h * p.dst_hs;
-    } else {
-        const int pg = s.seq_page[lt];
-        if (pg < 0) return false;
-        const bool isv = h >= p.n_dst + p.n_kv;
-        const long long at = (long long)pg * p.page_s + (long long)s.row[lt] * p.tok_s +
-                             (long long)(h - p.n_dst - (isv ? p.n_kv : 0)) * p.head_s;
-        d = static_cast<T*>(isv ? p.v : p.k) + at;
-    }
-    const T* x = static_cast<const T*>(p.src) + (t0 + lt) * p.src_ts + h * p.src_hs;
-    int a, b;
     it.cs = -1;
     it.n = it.n_turn = 2;
     const int rot = p.inv_freq ? p.rot : 0;
     if (turns && !p.interleaved && j * E < rot / 2) {
-        a = j * E;
-        b = a + rot / 2;
-        it.cs = lt * (rot / 2) + a;
+        it.a = j * E;
+        it.b = it.a + rot / 2;
+        it.cs = it.a;
     } else {
         // two consecutive vectors
-        a = turns && !p.interleaved ? rot + (j - rot / 2 / E) * 2 * E : j * 2 * E;
-        b = a + E;
-        if (turns && p.interleaved && a < rot) it.cs = lt * (rot / 2) + a / 2;
-        if (b >= rot) it.n_turn = 1;
-        if (b >= p.D) { it.n = 1; b = a; }
+        it.a = turns && !p.interleaved ? rot + (j - rot / 2 / E) * 2 * E : j * 2 * E;
+        it.b = it.a + E;
+        if (turns && p.interleaved && it.a < rot) it.cs = it.a / 2;
+        if (it.b >= rot) it.n_turn = 1;
+        if (it.b >= p.D) { it.n = 1; it.b = it.a; }
     }
-    it.src[0] = x + a; it.src[1] = x + b;
-    it.dst[0] = d + a; it.dst[1] = d + b;
-    return true;
+    return it;
 }
 
 template <class T, int E>
@@ -122,7 +118,7 @@ __device__ __forceinline__ void turn(const RopeParams& p, const float2* cs, cons
     if (!p.interleaved || E == 1) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const float2 c = cs[it.cs + e];
+            const float2 c = cs[e];
             const float x = to_f(a.e[e]), y = to_f(b.e[e]);
             a.e[e] = from_f<T>(fmaf(x, c.x, -(y * c.y)));
             b.e[e] = from_f<T>(fmaf(x, c.y, y * c.x));
@@ -135,7 +131,7 @@ __device__ __forceinline__ void turn(const RopeParams& p, const float2* cs, cons
             if (v >= it.n_turn) break;
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
-                const float2 c = cs[it.cs + v * (E / 2) + e / 2];
+                const float2 c = cs[v * (E / 2) + e / 2];
                 const float x = to_f(w.e[e]), y = to_f(w.e[e + 1]);
                 w.e[e] = from_f<T>(fmaf(x, c.x, -(y * c.y)));
                 w.e[e + 1] = from_f<T>(fmaf(x, c.y, y * c.x));
@@ -145,26 +141,42 @@ __device__ __forceinline__ void turn(const RopeParams& p, const float2* cs, cons
 }
 
 template <class T, int E>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p, int tpb, int ipr_rot,
-                                                        int ipr_copy) {
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p,
+                                                        const __grid_constant__ RopeShape g) {
     using V = typename VecOf<(int)sizeof(T) * E>::type;
     extern __shared__ __align__(16) float2 cs[];        // [tpb][rot / 2]
     __shared__ Smem s;
+    const long long t0 = (long long)blockIdx.x * g.tpb;
+    const int ntok = (int)min((long long)g.tpb, p.T - t0), items = ntok * g.per_tok;
     grid_dependency_wait();
     grid_launch_dependents();
-    const long long t0 = (long long)blockIdx.x * tpb;
-    const int ntok = (int)min((long long)tpb, p.T - t0);
+    // this thread's first items are on their way before anything else is known
+    Item it[kItems];
+    Vec<T, E> a[kItems], b[kItems];
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int u = 0; u < kItems; ++u) {
+            const int i = i0 + u * kThreads;
+            if (i < items) {
+                it[u] = item_of<E>(p, g, i);
+                const T* x = static_cast<const T*>(p.src) + (t0 + it[u].lt) * p.src_ts + it[u].h * p.src_hs;
+                a[u].raw = *reinterpret_cast<const V*>(x + it[u].a);
+                b[u].raw = *reinterpret_cast<const V*>(x + it[u].b);
+            }
+        }
+    };
+    load(threadIdx.x);
     if ((int)threadIdx.x < ntok) {
         const int i = threadIdx.x, t = (int)t0 + i;
         int live = 1, pos = 0, page = -1, row = 0;
         if (p.n_kv > 0) {
-            const int b = seq_of_row(p.q_starts, p.n_seqs, t);
-            live = b >= 0;
+            const int q = seq_of_row(p.q_starts, p.n_seqs, t);
+            live = q >= 0;
             if (live) {
-                const int place = __ldg(p.kv_lens + b) - __ldg(p.q_starts + b + 1) + t;
+                const int place = __ldg(p.kv_lens + q) - __ldg(p.q_starts + q + 1) + t;
                 pos = place;
                 if (place >= 0 && place / p.page < p.max_pages) {
-                    page = __ldg(p.table + (long long)b * p.max_pages + place / p.page);
+                    page = __ldg(p.table + (long long)q * p.max_pages + place / p.page);
                     row = place % p.page;
                     if (page >= p.n_pages) page = -1;
                 }
@@ -174,14 +186,6 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         s.live[i] = live; s.pos[i] = pos; s.seq_page[i] = page; s.row[i] = row;
     }
     __syncthreads();
-    Item it;
-    Vec<T, E> a, b;
-    int i = threadIdx.x;
-    bool have = find_item<T, E>(p, s, t0, ntok, i, ipr_rot, ipr_copy, it);
-    if (have) {
-        a.raw = *static_cast<const V*>(it.src[0]);
-        b.raw = *static_cast<const V*>(it.src[1]);
-    }
     const int half = p.inv_freq ? p.rot / 2 : 0;
     for (int k = threadIdx.x; k < ntok * half; k += kThreads) {
         const int lt = k / half;
@@ -191,22 +195,28 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         cs[k] = make_float2(c * p.magnitude, sn * p.magnitude);
     }
     __syncthreads();
-    const int per_tok = (p.H - p.n_kv - p.skip) * ipr_rot + p.n_kv * ipr_copy;
-    for (;;) {
-        if (have) {
-            const bool rot = it.cs >= 0;
-            if (rot) turn<T, E>(p, cs, it, a, b);
-            if (rot || p.copy_tail) {
-                *static_cast<V*>(it.dst[0]) = a.raw;
-                if (it.n == 2) *static_cast<V*>(it.dst[1]) = b.raw;
+    for (int i0 = threadIdx.x; i0 < items; i0 += kItems * kThreads) {
+        if (i0 != (int)threadIdx.x) load(i0);
+#pragma unroll
+        for (int u = 0; u < kItems; ++u) {
+            if (i0 + u * kThreads >= items || !s.live[it[u].lt]) continue;
+            const int lt = it[u].lt, h = it[u].h;
+            T* d;
+            if (h < p.n_dst) {
+                d = static_cast<T*>(p.dst) + (t0 + lt) * p.dst_ts + h * p.dst_hs;
+            } else {
+                const int pg = s.seq_page[lt];
+                if (pg < 0) continue;
+                const bool isv = h >= p.n_dst + p.n_kv;
+                d = static_cast<T*>(isv ? p.v : p.k) + (long long)pg * p.page_s + (long long)s.row[lt] * p.tok_s +
+                    (long long)(h - p.n_dst - (isv ? p.n_kv : 0)) * p.head_s;
             }
-        }
-        i += kThreads;
-        if (i >= ntok * per_tok) break;
-        have = find_item<T, E>(p, s, t0, ntok, i, ipr_rot, ipr_copy, it);
-        if (have) {
-            a.raw = *static_cast<const V*>(it.src[0]);
-            b.raw = *static_cast<const V*>(it.src[1]);
+            const bool rot = it[u].cs >= 0;
+            if (rot) turn<T, E>(p, cs + lt * half + it[u].cs, it[u], a[u], b[u]);
+            if (rot || p.copy_tail) {
+                *reinterpret_cast<V*>(d + it[u].a) = a[u].raw;
+                if (it[u].n == 2) *reinterpret_cast<V*>(d + it[u].b) = b[u].raw;
+            }
         }
     }
 }
@@ -219,15 +229,26 @@ template <class T, int E> cudaError_t launch_te(const RopeParams& p, cudaStream_
     const long long per_tok = (long long)(p.H - p.n_kv - p.skip) * ipr_rot + (long long)p.n_kv * ipr_copy;
     if (per_tok == 0) return cudaSuccess;
     if (per_tok > 0x3FFFFFF) return cudaErrorInvalidValue;
-    // tokens of a block: one item a thread; fewer when that would leave
-    // multiprocessors idle
-    long long tpb = kThreads / per_tok;
+    // tokens of a block: up to 3 items a thread; fewer when that would leave
+    // multiprocessors idle.  (One token a warp without block barriers, or
+    // blocks that walk over tokens with the next one's loads ahead, measured no
+    // faster: 8192 x 32 x 128 f16 rows 29-42 and 25-35 us.)
+    long long tpb = 3 * kThreads / per_tok;
     tpb = tpb < 1 ? 1 : tpb > kMaxTokens ? kMaxTokens : tpb;
     const long long fill = ((long long)p.T + api_sms() - 1) / api_sms();
     if (tpb > fill) tpb = fill;
     const long long grid = (p.T + tpb - 1) / tpb;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     const size_t smem = (size_t)tpb * (rot / 2) * sizeof(float2);
+    RopeShape g = {};
+    g.tpb = (int)tpb;
+    g.heads = p.H - p.n_kv - p.skip;
+    g.ipr_rot = ipr_rot;
+    g.ipr_copy = ipr_copy;
+    g.per_tok = (int)per_tok;
+    g.by_tok = make_div(per_tok, tpb * per_tok);
+    g.by_rot = make_div(ipr_rot, per_tok);
+    g.by_copy = make_div(ipr_copy, per_tok);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kThreads);
@@ -238,7 +259,7 @@ template <class T, int E> cudaError_t launch_te(const RopeParams& p, cudaStream_
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, rope_kernel<T, E>, p, (int)tpb, ipr_rot, ipr_copy);
+    return cudaLaunchKernelEx(&cfg, rope_kernel<T, E>, p, g);
 }
 
 template <class T> cudaError_t launch_t(const RopeParams& p, int vec_bytes, cudaStream_t st) {
