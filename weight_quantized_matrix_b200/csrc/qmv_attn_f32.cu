@@ -8,8 +8,8 @@
 //  * As in qmv_attn_few.cu every warp streams its own 16 keys of a tile through its
 //    own ring (cp.async, 16-byte chunks, XOR-swizzled).
 //  * Scores: lane = (key, half of the dims); a 16-byte read of the key serves up to
-//    16 rows, whose queries are broadcast reads.  Rows go in fours, and fours
-//    that the unit does not have are skipped.
+//    16 rows, whose queries are broadcast reads.  Units of up to 4, 8 or 16 rows
+//    run code of that size.
 //  * Weights go through shared memory; for the second product a lane owns D / 32
 //    dims of every row, V is read once for all rows.
 //  * DP = 64, 128 or 256 dims, padded with zeros in shared memory only.
@@ -39,19 +39,135 @@ template <int DP> struct F32Geom {
 };
 static_assert(kJoinBytes <= F32Geom<64>::RING, "joined in the ring");
 
-// 32 lanes x VEC dims: lane's dims are 4-float groups lane, lane + 32 (D = 256), or a pair (D = 64)
+// A unit's rows as the steps need them.
+struct Rows {
+    int lo[kRows], hi[kRows], pos[kRows];       // keys the row sees, its position
+    float slope[kRows];
+};
+
+// One step: 16 keys (j0 on) against the first R rows.  Scores with lane = (key,
+// half of the dims), weights through s_p, second product with lane = dims.
+template <int DP, bool MOD, int R>
+__device__ __forceinline__ void f32_step(const unsigned char* kb, const unsigned char* vb, const float* s_q, float (&s_p)[kRows][16],
+                                         const Rows& rows, const ScoreMod<true>& mod, int j0, bool full, float (&o)[kRows][DP / 32],
+                                         float (&m)[kRows], float (&l)[kRows]) {
+    using Gm = F32Geom<DP>;
+    constexpr int ROWB = Gm::ROWB, CPR = DP / 4, VEC = DP / 32;
+    const int lane = threadIdx.x & 31, key = lane & 15, hf = lane >> 4, j = j0 + key;
+    float x[R], mx[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) x[r] = 0.0f;
+#pragma unroll 2
+    for (int c = 0; c < CPR / 2; ++c) {
+        const float4 kv = *reinterpret_cast<const float4*>(kb + key * ROWB + (((hf * (CPR / 2) + c) ^ (key & 7)) << 4));
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float4 qv = *reinterpret_cast<const float4*>(s_q + (r * 2 + hf) * Gm::QH + c * 4);
+            x[r] = fmaf(qv.x, kv.x, x[r]);
+            x[r] = fmaf(qv.y, kv.y, x[r]);
+            x[r] = fmaf(qv.z, kv.z, x[r]);
+            x[r] = fmaf(qv.w, kv.w, x[r]);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        x[r] += __shfl_xor_sync(0xFFFFFFFFu, x[r], 16);
+        if constexpr (MOD) x[r] = mod.apply(x[r], rows.slope[r], j - rows.pos[r]);
+        else x[r] *= mod.pre;
+    }
+    if (!full) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (j < rows.lo[r] || j >= rows.hi[r]) x[r] = -INFINITY;
+    }
+    // all rows' maxima side by side: a butterfly's latency is paid once
+#pragma unroll
+    for (int r = 0; r < R; ++r) mx[r] = x[r];
+#pragma unroll
+    for (int w = 8; w > 0; w >>= 1)
+#pragma unroll
+        for (int r = 0; r < R; ++r) mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xFFFFFFFFu, mx[r], w));
+    bool raise = false;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        mx[r] = fmaxf(mx[r], m[r]);
+        raise |= mx[r] > m[r];
+    }
+    if (raise) {                                // the same for every lane
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float f = mx[r] > m[r] ? ex2(m[r] - mx[r]) : 1.0f;
+            l[r] *= f;
+#pragma unroll
+            for (int u = 0; u < VEC; ++u) o[r][u] *= f;
+            m[r] = mx[r];
+        }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const float e = ex2(x[r] - (mx[r] == -INFINITY ? 0.0f : mx[r]));
+        l[r] += e;                              // summed over the 16 lanes of a half at the end
+        if (hf == 0) s_p[r][key] = e;
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int k4 = 0; k4 < 16; k4 += 4) {
+        float v[4][VEC];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const unsigned char* row = vb + (k4 + k) * ROWB;
+            if constexpr (VEC == 2) {
+                const float2 f = *reinterpret_cast<const float2*>(row + (((lane >> 1) ^ ((k4 + k) & 7)) << 4) + (lane & 1) * 8);
+                v[k][0] = f.x; v[k][1] = f.y;
+            } else {
+#pragma unroll
+                for (int u = 0; u < VEC; u += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(row + (((lane + u * 8) ^ ((k4 + k) & 7)) << 4));
+                    v[k][u] = f.x; v[k][u + 1] = f.y; v[k][u + 2] = f.z; v[k][u + 3] = f.w;
+                }
+            }
+        }
+        if (full) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float4 w = *reinterpret_cast<const float4*>(&s_p[r][k4]);
+#pragma unroll
+                for (int u = 0; u < VEC; ++u) {
+                    o[r][u] = fmaf(w.x, v[0][u], o[r][u]);
+                    o[r][u] = fmaf(w.y, v[1][u], o[r][u]);
+                    o[r][u] = fmaf(w.z, v[2][u], o[r][u]);
+                    o[r][u] = fmaf(w.w, v[3][u], o[r][u]);
+                }
+            }
+        } else {
+            // a key the row does not see takes no part, whatever its value holds
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int jk = j0 + k4 + k;
+                    if (jk < rows.lo[r] || jk >= rows.hi[r]) continue;
+                    const float w = s_p[r][k4 + k];
+#pragma unroll
+                    for (int u = 0; u < VEC; ++u) o[r][u] = fmaf(w, v[k][u], o[r][u]);
+                }
+            }
+        }
+    }
+}
+
 template <int DP, bool MOD>
 __global__ void __launch_bounds__(F32Geom<DP>::WARPS * 32, F32Geom<DP>::PER_SM)
 attn_f32_kernel(const __grid_constant__ AttnParams p, int page_shift) {
     using Gm = F32Geom<DP>;
-    constexpr int WARPS = Gm::WARPS, NTH = WARPS * 32, STAGES = Gm::STAGES, ROWB = Gm::ROWB, CPR = DP / 4, VEC = DP / 32;
+    constexpr int WARPS = Gm::WARPS, NTH = WARPS * 32, STAGES = Gm::STAGES, ROWB = Gm::ROWB, CPR = DP / 4, VEC = DP / 32;           // a lane owns VEC dims
     extern __shared__ __align__(1024) unsigned char ring[];
     float* s_q = reinterpret_cast<float*>(ring + Gm::RING);
     __shared__ SchedSmem sm;
     __shared__ __align__(16) float s_p[WARPS][kRows][16];
     __shared__ float s_m[WARPS][kRows], s_l[WARPS][kRows];
-    __shared__ int s_lo[kRows], s_hi[kRows], s_pos[kRows];
-    __shared__ float s_slope[kRows];
+    __shared__ Rows rows;
     __shared__ int s_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned char* mine = ring + warp * STAGES * Gm::STEP;
@@ -133,15 +249,15 @@ attn_f32_kernel(const __grid_constant__ AttnParams p, int page_shift) {
         if (threadIdx.x < kRows) {
             const int r = threadIdx.x, pr = rbase + min(r, nrows - 1), ti = pr / p.G, h = sc.h * p.G + pr - ti * p.G;
             int lo, hi;
-            s_pos[r] = s.len - s.n + ti;
-            visible_keys(p, s_pos[r], s.len, lo, hi);
-            s_lo[r] = r < nrows ? lo : 0;
-            s_hi[r] = r < nrows ? hi : 0;
-            s_slope[r] = p.slopes ? __ldg(p.slopes + h) * kLog2e : 0.0f;
+            rows.pos[r] = s.len - s.n + ti;
+            visible_keys(p, rows.pos[r], s.len, lo, hi);
+            rows.lo[r] = r < nrows ? lo : 0;
+            rows.hi[r] = r < nrows ? hi : 0;
+            rows.slope[r] = p.slopes ? __ldg(p.slopes + h) * kLog2e : 0.0f;
         }
         __syncthreads();
         // keys that every row sees (bounds ascend with the row)
-        const int alo = s_lo[nrows - 1], ahi = s_hi[0];
+        const int alo = rows.lo[nrows - 1], ahi = rows.hi[0];
 
         float o[kRows][VEC], m[kRows], l[kRows];
 #pragma unroll
@@ -169,95 +285,10 @@ attn_f32_kernel(const __grid_constant__ AttnParams p, int page_shift) {
             if (j0 >= uhi || j0 + 16 <= ulo) continue;
             const bool full = j0 >= alo && j0 + 16 <= ahi;
 
-            // ---- scores: lane = (key, half of the dims) -------------------------
-            const int key = lane & 15, hf = lane >> 4, j = j0 + key;
-            float x[kRows];
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) x[r] = 0.0f;
-#pragma unroll 2
-            for (int c = 0; c < CPR / 2; ++c) {
-                const float4 kv = *reinterpret_cast<const float4*>(kb + key * ROWB + (((hf * (CPR / 2) + c) ^ (key & 7)) << 4));
-#pragma unroll
-                for (int g = 0; g < kRows; g += 4) {
-                    if (g < nrows) {
-#pragma unroll
-                        for (int r = g; r < g + 4; ++r) {
-                            const float4 qv = *reinterpret_cast<const float4*>(s_q + (r * 2 + hf) * Gm::QH + c * 4);
-                            x[r] = fmaf(qv.x, kv.x, x[r]);
-                            x[r] = fmaf(qv.y, kv.y, x[r]);
-                            x[r] = fmaf(qv.z, kv.z, x[r]);
-                            x[r] = fmaf(qv.w, kv.w, x[r]);
-                        }
-                    }
-                }
-            }
-            // ---- softmax ----------------------------------------------------------
-            __syncwarp();
-#pragma unroll
-            for (int g = 0; g < kRows; g += 4) {
-                if (g < nrows) {
-#pragma unroll
-                    for (int r = g; r < g + 4; ++r) {
-                        x[r] += __shfl_xor_sync(0xFFFFFFFFu, x[r], 16);
-                        if constexpr (MOD) x[r] = mod.apply(x[r], s_slope[r], j - s_pos[r]);
-                        else x[r] *= mod.pre;
-                        if (!full && (j < s_lo[r] || j >= s_hi[r])) x[r] = -INFINITY;
-                        float mx = x[r];
-#pragma unroll
-                        for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, w));
-                        mx = fmaxf(mx, m[r]);
-                        const float base = mx == -INFINITY ? 0.0f : mx;
-                        if (mx > m[r]) {
-                            const float f = ex2(m[r] - base);
-                            l[r] *= f;
-#pragma unroll
-                            for (int u = 0; u < VEC; ++u) o[r][u] *= f;
-                            m[r] = mx;
-                        }
-                        const float e = ex2(x[r] - base);
-                        l[r] += e;                       // keys are held twice: halved at the end
-                        if (hf == 0) s_p[warp][r][key] = e;
-                    }
-                }
-            }
-            __syncwarp();
-            // ---- O += P V: lane = dims ---------------------------------------------
-#pragma unroll 1
-            for (int k4 = 0; k4 < 16; k4 += 4) {
-                float v[4][VEC];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const unsigned char* row = vb + (k4 + k) * ROWB;
-                    if constexpr (VEC == 2) {
-                        const float2 f = *reinterpret_cast<const float2*>(row + (((lane >> 1) ^ ((k4 + k) & 7)) << 4) + (lane & 1) * 8);
-                        v[k][0] = f.x; v[k][1] = f.y;
-                    } else {
-#pragma unroll
-                        for (int u = 0; u < VEC; u += 4) {
-                            const float4 f = *reinterpret_cast<const float4*>(row + (((lane + u * 8) ^ ((k4 + k) & 7)) << 4));
-                            v[k][u] = f.x; v[k][u + 1] = f.y; v[k][u + 2] = f.z; v[k][u + 3] = f.w;
-                        }
-                    }
-                }
-#pragma unroll
-                for (int g = 0; g < kRows; g += 4) {
-                    if (g < nrows) {
-#pragma unroll
-                        for (int r = g; r < g + 4; ++r) {
-                            const float4 w = *reinterpret_cast<const float4*>(&s_p[warp][r][k4]);
-                            const float pw[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                // a key the row does not see takes no part, whatever its value holds
-                                if (full || (j0 + k4 + k >= s_lo[r] && j0 + k4 + k < s_hi[r])) {
-#pragma unroll
-                                    for (int u = 0; u < VEC; ++u) o[r][u] = fmaf(pw[k], v[k][u], o[r][u]);
-                                }
-                            }
-                        }
-                    }
-                }
-            }
+            // as many rows as the unit has, in fours
+            if (nrows <= 4) f32_step<DP, MOD, 4>(kb, vb, s_q, s_p[warp], rows, mod, j0, full, o, m, l);
+            else if (nrows <= 8) f32_step<DP, MOD, 8>(kb, vb, s_q, s_p[warp], rows, mod, j0, full, o, m, l);
+            else f32_step<DP, MOD, 16>(kb, vb, s_q, s_p[warp], rows, mod, j0, full, o, m, l);
         }
         cp_wait<0>();
         __syncthreads();

@@ -158,7 +158,8 @@ template <int ROWS, int TK> struct Sched {
         split = p.partials != nullptr;
         live = false;
         Q = 1;
-        int v = 0, pass = 0;    // 0: count tiles, 1: parts end with their units, 2: they do not
+        int v = 0, pass = 0;    // 0: count tiles, 1..4: parts of each, 5/4, 3/2, 2 times each tiles end with their units, 5: they do not
+        int each = 0;           // tiles a block
         long long incl = 0, all;
 #pragma unroll 1
         for (;;) {
@@ -174,24 +175,24 @@ template <int ROWS, int TK> struct Sched {
                 if (all == 0) return;
                 if (all >> 30) {
                     Q = (int)(all >> 29) + 1;
-                    pass = 2;
+                    pass = 5;
                     continue;
                 }
-                const int each = (int)(((unsigned)all + gridDim.x - 1) / gridDim.x);
+                each = (int)(((unsigned)all + gridDim.x - 1) / gridDim.x);
                 if (split && each <= kAlignTiles) {
                     Q = max(each, min_tiles);
                     pass = 1;
                     continue;
                 }
-            } else if (pass == 1 && all > (long long)gridDim.x) {
-                Q = 1;
-                pass = 2;
+            } else if (pass < 5 && all > (long long)gridDim.x) {
+                ++pass;
+                Q = pass == 5 ? 1 : max(min_tiles, each * (pass == 4 ? 8 : pass + 3) / 4);
                 continue;
             }
             break;
         }
         W = (int)all;
-        nblk = pass == 1 ? W : min((int)gridDim.x, max(1, Q == 1 ? W / min_tiles : W));
+        nblk = pass >= 1 && pass < 5 ? W : min((int)gridDim.x, max(1, Q == 1 ? W / min_tiles : W));
         if ((int)blockIdx.x >= nblk) return;
         q = W / nblk;
         rem = W - q * nblk;
