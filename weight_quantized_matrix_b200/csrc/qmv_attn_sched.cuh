@@ -10,9 +10,11 @@
 // other lengths).  Each block finds its own part: it sums the units' tile
 // counts over the sequences with a block-wide scan.
 //
-// Few tiles a block are cut at the units' own ends instead (every unit into
-// parts of Q tiles, the last one shorter), as long as that gives no more parts
-// than blocks: a block that ends one unit and begins another pays two joins.
+// A block that ends one unit and begins another pays two joins, of about ten
+// tiles' time each.  Few tiles a block are therefore cut at the units' own ends
+// (every unit into parts of Q tiles, the last one shorter), as long as some Q up to
+// twice the even share gives no more parts than blocks; failing that, in
+// quarters of the even share, so that short units stay whole.
 //
 // A block whose part ends or begins inside a unit leaves that unit's partial
 // result (unnormalised sums, maxima, weights) in the workspace and counts
@@ -186,13 +188,13 @@ template <int ROWS, int TK> struct Sched {
                 }
             } else if (pass < 5 && all > (long long)gridDim.x) {
                 ++pass;
-                Q = pass == 5 ? 1 : max(min_tiles, each * (pass == 4 ? 8 : pass + 3) / 4);
+                Q = pass == 5 ? max(4, each / 4) : max(min_tiles, each * (pass == 4 ? 8 : pass + 3) / 4);
                 continue;
             }
             break;
         }
         W = (int)all;
-        nblk = pass >= 1 && pass < 5 ? W : min((int)gridDim.x, max(1, Q == 1 ? W / min_tiles : W));
+        nblk = pass >= 1 && pass < 5 ? W : min((int)gridDim.x, W);
         if ((int)blockIdx.x >= nblk) return;
         q = W / nblk;
         rem = W - q * nblk;
