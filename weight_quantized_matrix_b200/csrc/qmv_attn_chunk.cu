@@ -625,6 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
             const float inv = empty ? 0.0f : 1.0f / l;
             const long long row = pc->t0 + ti;
             T* out = static_cast<T*>(p.out) + row * p.o_ts + (long long)head * p.o_hs;
+            // a partial result holds 4 dims of all rows side by side: lanes are rows
             const size_t ss = (size_t)kRows * (p.D + 2);
             const int at = h * kHalf + r;                // row of the unit
             float* so = p.partials + pc->slot * ss;
@@ -644,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
 #pragma unroll
                     for (int u = 0; u < 16; u += 4)
                         if (c + u < p.D)
-                            __stcg(reinterpret_cast<float4*>(so + (size_t)at * p.D + c + u), make_float4(o[u], o[u + 1], o[u + 2], o[u + 3]));
+                            __stcg(reinterpret_cast<float4*>(so) + (size_t)((c + u) / 4) * kRows + at, make_float4(o[u], o[u + 1], o[u + 2], o[u + 3]));
                 } else if (mine) {
                     put16<T>(out + c, o, inv, p.D - c, g.out_vec);
                 }
@@ -674,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                 for (int i = 0; i < DP / 32; ++i) {
                     const int d = lane + 32 * i;
                     if (d >= p.D) continue;
-                    if (part) __stcg(so + (size_t)sat * p.D + d, sl == 0.0f ? 0.0f : o[i]);
+                    if (part) __stcg(so + ((size_t)(d / 4) * kRows + sat) * 4 + d % 4, sl == 0.0f ? 0.0f : o[i]);
                     else st_elem(static_cast<T*>(p.out) + srow * p.o_ts + (long long)shead * p.o_hs + d, sl == 0.0f ? 0.0f : o[i] / sl);
                 }
                 if (lane == 0 && part) {
@@ -716,15 +717,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                             float o[16];
 #pragma unroll
                             for (int u = 0; u < 16; ++u) o[u] = 0.0f;
-#pragma unroll 1
+#pragma unroll 2
                             for (int c = c0; c <= c1; ++c) {
-                                const float* sp = p.partials + slot(c) + (size_t)at * p.D + d;
+                                const float4* sp = reinterpret_cast<const float4*>(p.partials + slot(c)) + (size_t)(d / 4) * kRows + at;
                                 const float pl = __ldcg(st + slot(c) + kRows);
                                 const float f = part_weight(__ldcg(st + slot(c)), pl, M);
 #pragma unroll
                                 for (int u = 0; u < 16; u += 4)
                                     if (d + u < p.D) {
-                                        const float4 v4 = __ldcg(reinterpret_cast<const float4*>(sp + u));
+                                        const float4 v4 = __ldcg(sp + (size_t)(u / 4) * kRows);
                                         o[u] = fmaf(v4.x, f, o[u]); o[u + 1] = fmaf(v4.y, f, o[u + 1]);
                                         o[u + 2] = fmaf(v4.z, f, o[u + 2]); o[u + 3] = fmaf(v4.w, f, o[u + 3]);
                                     }
