@@ -58,7 +58,7 @@ template <bool EXACT> struct ScoreMod {
         if (cap) {
             float big = 0.0f;
 #pragma unroll
-            for (int c = 0; c < N; ++c) big = fmaxf(big, fabsf(x[c]));
+            for (int c = 0; c < N; c += 2) big = max3(fabsf(x[c]), fabsf(x[c + 1]), big);
             const float half = pre * (0.5f * kLn2);             // pre holds 2 log2 e / c
             if (__all_sync(0xFFFFFFFFu, big * half <= 0.7f)) {
                 const float2 h2 = make_float2(half, half), post2 = make_float2(post, post);
@@ -87,8 +87,13 @@ template <bool EXACT> struct ScoreMod {
         }
         if (slope_log2 != 0.0f) {
             const float a0 = (float)away;
+            const float2 a2 = make_float2(a0, a0), s2 = make_float2(slope_log2, slope_log2);
 #pragma unroll
-            for (int c = 0; c < N; ++c) x[c] = fmaf(slope_log2, a0 + (float)c, x[c]);
+            for (int c = 0; c < N; c += 2) {
+                const float2 v = fma2(s2, add2(a2, make_float2((float)c, (float)(c + 1))), make_float2(x[c], x[c + 1]));
+                x[c] = v.x;
+                x[c + 1] = v.y;
+            }
         }
     }
 };
