@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                     if (npiece > 0 && !warp_wait_all(wait, s_addr(&bars.q_empty), (uint32_t)(npiece - 1) & 1u)) break;
 #pragma unroll 1
                     for (int gr = w; gr < kRows / 8; gr += kLoaders) {
-                        const int r = gr * 8 + (lane & 7), pr = rbase + min(r, nrows - 1), ti = pr / p.G;
+                        const int r = gr * 8 + (lane & 7), pr = rbase + min(r, nrows - 1), ti = token_of(p, pr);
                         const long long off = ((long long)(pc->t0 + ti) * p.q_ts + (long long)(hk * p.G + pr - ti * p.G) * p.q_hs) * 2;
 #pragma unroll
                         for (int u = 0; u < PER; ++u) {
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
             float slope = 0.0f;
             if (r < nrows) {
                 const int pr = rbase + r;
-                ti = pr / p.G;
+                ti = token_of(p, pr);
                 head = pc->h * p.G + pr - ti * p.G;
                 pos = pc->len - pc->n + ti;
                 visible_keys(p, pos, pc->len, lo, hi);

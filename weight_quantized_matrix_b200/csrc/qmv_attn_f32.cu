@@ -239,7 +239,7 @@ attn_f32_kernel(const __grid_constant__ AttnParams p, int page_shift) {
 
         // ---- queries and the rows' keys --------------------------------------
         for (int x = threadIdx.x; x < kRows * CPR; x += NTH) {
-            const int r = x / CPR, c = x % CPR, pr = rbase + min(r, nrows - 1), ti = pr / p.G;
+            const int r = x / CPR, c = x % CPR, pr = rbase + min(r, nrows - 1), ti = token_of(p, pr);
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (r < nrows && c < chunks)
                 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + (long long)(s.t0 + ti) * p.q_ts +
@@ -247,7 +247,7 @@ attn_f32_kernel(const __grid_constant__ AttnParams p, int page_shift) {
             *reinterpret_cast<float4*>(s_q + (r * 2 + c / (CPR / 2)) * Gm::QH + c % (CPR / 2) * 4) = v;
         }
         if (threadIdx.x < kRows) {
-            const int r = threadIdx.x, pr = rbase + min(r, nrows - 1), ti = pr / p.G, h = sc.h * p.G + pr - ti * p.G;
+            const int r = threadIdx.x, pr = rbase + min(r, nrows - 1), ti = token_of(p, pr), h = sc.h * p.G + pr - ti * p.G;
             int lo, hi;
             rows.pos[r] = s.len - s.n + ti;
             visible_keys(p, rows.pos[r], s.len, lo, hi);
@@ -313,7 +313,7 @@ attn_f32_kernel(const __grid_constant__ AttnParams p, int page_shift) {
         const bool part = sc.shared();
         float* slot_o = part ? attn_slot(p, blockIdx.x, sc.w0 >= sc.us ? 0 : 1, kRows) : nullptr;
         auto store = [&](int r, int d, float4 v, float mm, float ll) {
-            const int pr = rbase + r, ti = pr / p.G, h = sc.h * p.G + pr - ti * p.G;
+            const int pr = rbase + r, ti = token_of(p, pr), h = sc.h * p.G + pr - ti * p.G;
             const long long row = s.t0 + ti;
             if (ll == 0.0f) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;

@@ -28,28 +28,29 @@ namespace qmv {
 
 namespace {
 
-constexpr int kWarps = 4;
 constexpr int kRows = 16;
-constexpr int kTile = 64;            // keys of a tile, 16 a warp
 
-template <int DP> struct FewGeom {
+// WARPS 4: two blocks an SM (one at DP = 256); 8: one, for batches of fewer units
+// than SMs, whose blocks then take 128 keys a step.
+template <int DP, int WARPS> struct FewGeom {
+    static constexpr int TILE = 16 * WARPS;                // keys of a tile, 16 a warp
     static constexpr int STAGES = DP == 64 ? 6 : 3;
-    static constexpr int PER_SM = DP == 256 ? 1 : 2;
+    static constexpr int PER_SM = DP == 256 || WARPS == 8 ? 1 : 2;
     static constexpr int ROWB = DP * 2;                    // bytes of a key in shared memory
     static constexpr int STEP = 2 * 16 * ROWB;             // a warp's K and V of one tile
-    static constexpr int RING = kWarps * STAGES * STEP;
+    static constexpr int RING = WARPS * STAGES * STEP;
 };
-static_assert(kWarps * kRows * 256 * 4 <= FewGeom<256>::RING && kWarps * kRows * 64 * 4 <= FewGeom<64>::RING, "joined in the ring");
-static_assert(kJoinBytes <= FewGeom<64>::RING, "joined in the ring");
+static_assert(4 * kRows * 256 * 4 <= FewGeom<256, 4>::RING && 4 * kRows * 64 * 4 <= FewGeom<64, 4>::RING, "joined in the ring");
+static_assert(kJoinBytes <= FewGeom<64, 4>::RING, "joined in the ring");
 
-template <class T, int DP, bool MOD>
-__global__ void __launch_bounds__(kWarps * 32, FewGeom<DP>::PER_SM) attn_few_kernel(const __grid_constant__ AttnParams p,
-                                                                                 int page_shift) {
-    using Gm = FewGeom<DP>;
+template <class T, int DP, int WARPS, bool MOD>
+__global__ void __launch_bounds__(WARPS * 32, FewGeom<DP, WARPS>::PER_SM) attn_few_kernel(const __grid_constant__ AttnParams p,
+                                                                                       int page_shift) {
+    using Gm = FewGeom<DP, WARPS>;
     constexpr int STAGES = Gm::STAGES, ROWB = Gm::ROWB, KS = DP / 16, NT = DP / 8, CPR = DP / 8;
     extern __shared__ __align__(1024) unsigned char ring[];
     __shared__ SchedSmem sm;
-    __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+    __shared__ float s_m[WARPS][kRows], s_l[WARPS][kRows];
     __shared__ int s_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gid = lane >> 2, tig = lane & 3;
@@ -59,8 +60,8 @@ __global__ void __launch_bounds__(kWarps * 32, FewGeom<DP>::PER_SM) attn_few_ker
     grid_dependency_wait();
     grid_launch_dependents();
 
-    Sched<kRows, kTile> sc;
-    sc.init<kWarps * 32, 1>(p, sm, 12);
+    Sched<kRows, Gm::TILE> sc;
+    sc.template init<WARPS * 32, 1>(p, sm, 768 / Gm::TILE);
     const ScoreMod<false> mod(p);
     const float scale2 = p.scale * kLog2e;
     const int page16 = (int)(p.page_s / 8), tok16 = (int)(p.tok_s / 8);
@@ -80,7 +81,7 @@ __global__ void __launch_bounds__(kWarps * 32, FewGeom<DP>::PER_SM) attn_few_ker
         // lanes r and r + 16: place of key r of this warp's step t, in units of 16
         // bytes; -1 outside the unit's keys, -2 on a bad page
         auto place = [&](int t) -> int {
-            const int j = t * kTile + warp * 16 + (lane & 15);
+            const int j = t * Gm::TILE + warp * 16 + (lane & 15);
             if (t >= k1 || j < ulo || j >= uhi) return -1;
             const int e = page_shift >= 0 ? j >> page_shift : j / p.page;
             if (e >= p.max_pages) return -2;
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(kWarps * 32, FewGeom<DP>::PER_SM) attn_few_ker
         for (int e = 0; e < 2; ++e) {
             const int r = gid + 8 * e;
             const bool in = r < nrows;
-            const int pr = rbase + (in ? r : 0), ti = pr / p.G, h = sc.h * p.G + pr - ti * p.G;
+            const int pr = rbase + (in ? r : 0), ti = token_of(p, pr), h = sc.h * p.G + pr - ti * p.G;
             pos[e] = s.len - s.n + ti;
             visible_keys(p, pos[e], s.len, lo[e], hi[e]);
             if (!in) lo[e] = hi[e] = 0;
@@ -188,7 +189,7 @@ __global__ void __launch_bounds__(kWarps * 32, FewGeom<DP>::PER_SM) attn_few_ker
             if (t < k0) continue;
             const uint32_t kb = mine_a + slot * Gm::STEP, vb = kb + 16 * ROWB;
             slot = slot + 1 == STAGES ? 0 : slot + 1;
-            const int j0 = t * kTile + warp * 16;
+            const int j0 = t * Gm::TILE + warp * 16;
             if (j0 >= uhi || j0 + 16 <= ulo) continue;
 
             // ---- S = Q K^T: 16 rows x 16 keys ---------------------------------
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(kWarps * 32, FewGeom<DP>::PER_SM) attn_few_ker
         const bool part = sc.shared();
         float* slot_o = part ? attn_slot(p, blockIdx.x, sc.w0 >= sc.us ? 0 : 1, kRows) : nullptr;
         auto store = [&](int r, int d, float4 v, float mm, float ll) {
-            const int pr = rbase + r, ti = pr / p.G, h = sc.h * p.G + pr - ti * p.G;
+            const int pr = rbase + r, ti = token_of(p, pr), h = sc.h * p.G + pr - ti * p.G;
             const long long row = s.t0 + ti;
             const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;    // no key: 0 even where a sum is not a number
             if (ll == 0.0f) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -323,16 +324,16 @@ __global__ void __launch_bounds__(kWarps * 32, FewGeom<DP>::PER_SM) attn_few_ker
             if (d == 0 && p.lse) p.lse[row * p.Hq + h] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
         };
 #pragma unroll 1
-        for (int x = threadIdx.x; x < nrows * (DP / 4); x += kWarps * 32) {
+        for (int x = threadIdx.x; x < nrows * (DP / 4); x += WARPS * 32) {
             const int r = x / (DP / 4), d = (x % (DP / 4)) * 4;
             if (d >= p.D) continue;
             float mm = s_m[0][r];
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, s_m[w][r]);
+            for (int w = 1; w < WARPS; ++w) mm = fmaxf(mm, s_m[w][r]);
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             float ll = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
+            for (int w = 0; w < WARPS; ++w) {
                 const float f = part_weight(s_m[w][r], s_l[w][r], mm);
                 const float4 u = *reinterpret_cast<const float4*>(red + (w * kRows + r) * DP + d);
                 v.x = fmaf(u.x, f, v.x); v.y = fmaf(u.y, f, v.y); v.z = fmaf(u.z, f, v.z); v.w = fmaf(u.w, f, v.w);
@@ -345,16 +346,16 @@ __global__ void __launch_bounds__(kWarps * 32, FewGeom<DP>::PER_SM) attn_few_ker
                 store(r, d, v, mm, ll);
             }
         }
-        if (part && attn_arrive(p, sc, &s_flag)) attn_join<kWarps * 32>(p, sc, nrows, ring, store);
+        if (part && attn_arrive(p, sc, &s_flag)) attn_join<WARPS * 32>(p, sc, nrows, ring, store);
         __syncthreads();
         sc.next(p);
     }
 }
 
-template <class T, int DP, bool MOD> cudaError_t launch_tdm(const AttnParams& p, cudaStream_t st) {
-    using Gm = FewGeom<DP>;
+template <class T, int DP, int WARPS, bool MOD> cudaError_t launch_tdm(const AttnParams& p, cudaStream_t st) {
+    using Gm = FewGeom<DP, WARPS>;
     static std::atomic<unsigned> configured{0};
-    auto kern = attn_few_kernel<T, DP, MOD>;
+    auto kern = attn_few_kernel<T, DP, WARPS, MOD>;
     int shift = -1;
     if ((p.page & (p.page - 1)) == 0)
         for (shift = 0; (1 << shift) < p.page; ++shift) {}
@@ -369,7 +370,7 @@ template <class T, int DP, bool MOD> cudaError_t launch_tdm(const AttnParams& p,
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(std::min(api_sms(), 148) * Gm::PER_SM));
-    cfg.blockDim = dim3(kWarps * 32);
+    cfg.blockDim = dim3(WARPS * 32);
     cfg.dynamicSmemBytes = Gm::RING;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -380,18 +381,29 @@ template <class T, int DP, bool MOD> cudaError_t launch_tdm(const AttnParams& p,
     return cudaLaunchKernelEx(&cfg, kern, p, shift);
 }
 
-template <class T, int DP> cudaError_t launch_td(const AttnParams& p, cudaStream_t st) {
-    return p.softcap > 0.0f || p.slopes ? launch_tdm<T, DP, true>(p, st) : launch_tdm<T, DP, false>(p, st);
+template <class T, int DP, int WARPS> cudaError_t launch_tdw(const AttnParams& p, cudaStream_t st) {
+    return p.softcap > 0.0f || p.slopes ? launch_tdm<T, DP, WARPS, true>(p, st) : launch_tdm<T, DP, WARPS, false>(p, st);
 }
 
-template <class T> cudaError_t launch_t(const AttnParams& p, cudaStream_t st) {
-    return p.D <= 64 ? launch_td<T, 64>(p, st) : p.D <= 128 ? launch_td<T, 128>(p, st) : launch_td<T, 256>(p, st);
+template <class T, int DP> cudaError_t launch_td(const AttnParams& p, long long units, cudaStream_t st) {
+    if constexpr (DP < 256) {
+        // Fewer units than SMs: a short call's time is its steps' latency, and 8
+        // warps halve the steps (517 keys: 12.4 us, 15.5 with 4); a long one has fewer
+        // parts to join.  More units: two blocks an SM fill each other's gaps.
+        if (units <= api_sms()) return launch_tdw<T, DP, 8>(p, st);
+    }
+    return launch_tdw<T, DP, 4>(p, st);
+}
+
+template <class T> cudaError_t launch_t(const AttnParams& p, long long units, cudaStream_t st) {
+    return p.D <= 64 ? launch_td<T, 64>(p, units, st) : p.D <= 128 ? launch_td<T, 128>(p, units, st) : launch_td<T, 256>(p, units, st);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_few(int dtype, const AttnParams& p, cudaStream_t st) {
-    return dtype == 1 ? launch_t<__half>(p, st) : launch_t<__nv_bfloat16>(p, st);
+cudaError_t launch_attn_few(int dtype, const AttnParams& p, int max_q_len, cudaStream_t st) {
+    const long long units = (long long)p.n_seqs * p.Hkv * (((long long)max_q_len * p.G + kRows - 1) / kRows);
+    return dtype == 1 ? launch_t<__half>(p, units, st) : launch_t<__nv_bfloat16>(p, units, st);
 }
 
 }  // namespace qmv

@@ -47,8 +47,8 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int b) {
 // Keys [lo, hi) that any of the packed rows r0..r1 of a sequence sees (0, 0: none).
 __device__ __forceinline__ void rows_keys(const AttnParams& p, const SeqInfo& s, int r0, int r1, int& lo, int& hi) {
     int x;
-    visible_keys(p, s.len - s.n + r0 / p.G, s.len, lo, x);
-    visible_keys(p, s.len - s.n + r1 / p.G, s.len, x, hi);
+    visible_keys(p, s.len - s.n + token_of(p, r0), s.len, lo, x);
+    visible_keys(p, s.len - s.n + token_of(p, r1), s.len, x, hi);
     if (lo >= hi) lo = hi = 0;
 }
 

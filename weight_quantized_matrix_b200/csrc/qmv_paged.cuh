@@ -58,6 +58,7 @@ struct AttnParams {
     long long q_ts, q_hs, o_ts, o_hs;
     long long page_s, tok_s, head_s;
     int T, Hq, Hkv, G, D;
+    unsigned g_mul;                 // ceil(2^32 / G) where rows / G is exact by it, else 0
     int n_seqs, n_pages, page, max_pages;
     int causal, window;             // window 0: none
     float scale, softcap;           // softcap 0: none
@@ -94,6 +95,11 @@ __device__ __forceinline__ void visible_keys(const AttnParams& p, int pos, int l
     if (hi < 0) hi = 0;
 }
 
+// Packed row r (new token r / G, head r % G of its kv head) -> token.
+__device__ __forceinline__ int token_of(const AttnParams& p, int r) {
+    return p.g_mul ? (int)__umulhi((unsigned)r, p.g_mul) : p.G == 1 ? r : r / p.G;
+}
+
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -126,7 +132,7 @@ inline cudaError_t launch_dependent(Kern kern, std::atomic<unsigned>& configured
 }
 
 cudaError_t launch_rope(int dtype, const RopeParams& p, int vec_bytes, cudaStream_t st);
-cudaError_t launch_attn_few(int dtype, const AttnParams& p, cudaStream_t st);
+cudaError_t launch_attn_few(int dtype, const AttnParams& p, int max_q_len, cudaStream_t st);
 cudaError_t launch_attn_chunk(int dtype, const AttnParams& p, cudaStream_t st);
 cudaError_t launch_attn_f32(const AttnParams& p, cudaStream_t st);
 cudaError_t launch_attn_rows(int dtype, const AttnParams& p, cudaStream_t st);

@@ -220,6 +220,8 @@ int qmv_paged_attention(const void* q, const qmv_paged_kv* kv, void* out, float*
     p.page_s = kv->page_stride; p.tok_s = kv->token_stride; p.head_s = kv->head_stride;
     p.T = T; p.Hq = n_q_heads; p.Hkv = kv->n_kv_heads; p.G = n_q_heads / kv->n_kv_heads; p.D = D;
     p.n_seqs = kv->n_seqs; p.n_pages = kv->n_pages; p.page = kv->page_size; p.max_pages = kv->max_pages;
+    // exact for r G < 2^32 (G > 1; r < T G)
+    if (p.G > 1 && (long long)T * p.G * p.G < (1LL << 32)) p.g_mul = (unsigned)((1ULL << 32) / p.G + 1);
     p.causal = causal;
     p.window = window > (1 << 30) ? 0 : window;      // wider than any position: none
     p.scale = scale; p.softcap = softcap;
@@ -240,9 +242,9 @@ int qmv_paged_attention(const void* q, const qmv_paged_kv* kv, void* out, float*
     if (vec == 16 && near) {
         p.fault = qmv::api_fault_word();
         if (!p.fault) return QMV_ECUDA;
-        const long long rows = (long long)(max_q_len > 0 && max_q_len < T ? max_q_len : T) * p.G;
-        if (rows > 16 && D <= 128) return qmv::api_finish(qmv::launch_attn_chunk(kv->dtype, p, s));
-        return qmv::api_finish(qmv::launch_attn_few(kv->dtype, p, s));
+        const int most = max_q_len > 0 && max_q_len < T ? max_q_len : T;
+        if ((long long)most * p.G > 16 && D <= 128) return qmv::api_finish(qmv::launch_attn_chunk(kv->dtype, p, s));
+        return qmv::api_finish(qmv::launch_attn_few(kv->dtype, p, most, s));
     }
     return qmv::api_finish(qmv::launch_attn_rows(kv->dtype, p, s));
 }
