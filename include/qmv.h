@@ -604,8 +604,9 @@ int qmv_describe_plan(int family, int M, int N, int K, int bits, int group_size,
  * stream weights through a shared-memory ring wait on barriers with a bound
  * (about one second); a wait that expires ORs a nonzero code into this word
  * (1: a consumer warp gave up on a ring stage, 2: the producer warp gave up on
- * a free stage, 4: the producer gave up waiting for its own copies) and the
- * call that hit it leaves y undefined.  Writes the word to *code and, if clear != 0,
+ * a free stage, 4: the producer gave up waiting for its own copies, 8 and 16:
+ * the warps that issue products or hand out work) and the call that hit it
+ * leaves y (out, lse) undefined, and an attention workspace to be cleared.  Writes the word to *code and, if clear != 0,
  * resets it to zero.  Synchronous: it waits for the device's pending work
  * (cudaMemcpyFromSymbol).  Returns QMV_OK, QMV_EINVAL (code NULL) or QMV_ECUDA.
  */
@@ -643,7 +644,9 @@ void qmv_force_config(int path, int rows_per_warp, int warps_k, int warps_rows);
  * consumer warps then give up their bounded wait on the stage (about 1 s) and
  * OR code 1 into the fault word, the producer gives up its wait for its own
  * copies on it and ORs code 4, and the kernel returns normally with undefined
- * output; no copy is left in flight, and the context stays usable.  Process
+ * output; no copy is left in flight, and the context stays usable.  Likewise
+ * qmv_paged_attention's kernel for many rows leaves out block 0's first tile of
+ * keys: one or more of its warps give up (codes 1, 2, 8, 16).  Process
  * global, not thread-safe; 0 restores normal launches.
  */
 void qmv_test_skip_last_copy(int enable);

@@ -160,8 +160,19 @@ def attention64(bt: Batch, scale=None, causal=True, window=0, cap=0.0, slopes=No
     return out, lse, tol, tol_l
 
 
+def wide_table(bt: Batch):
+    """The page table with so many (unused) columns that the call is taken for
+    one over long sequences: many query rows then run on the kernel for them,
+    which short calls leave to the one for few."""
+    units = len(bt.new) * bt.Hkv
+    cols = max(bt.max_pages, -(-4000 * 64 // (bt.page * units)) + 1)
+    t = torch.full((len(bt.new), cols), -1, dtype=torch.int32)
+    t[:, :bt.max_pages] = bt.table
+    return t
+
+
 def run_attention(q, bt: Batch, workspace=None, max_q_len=None, lse=True, k=None, v=None, q_strided=False, stream=None,
-                  **kw):
+                  wide=False, **kw):
     dt = TORCH_DT[bt.dtype]
     fill = 7.0
     if q_strided:                     # the query heads inside a fused [Q | K | V] row
@@ -175,10 +186,11 @@ def run_attention(q, bt: Batch, workspace=None, max_q_len=None, lse=True, k=None
     ls = torch.full((bt.T, bt.Hq), fill, dtype=torch.float32, device="cuda") if lse else None
     slopes = kw.pop("slopes", None)
     sl = None if slopes is None else torch.tensor(slopes, dtype=torch.float32, device="cuda")
-    keep = [bt.cache(bt.k) if k is None else k, bt.cache(bt.v) if v is None else v, bt.table.cuda(), bt.starts.cuda(),
+    table = wide_table(bt) if wide else bt.table
+    keep = [bt.cache(bt.k) if k is None else k, bt.cache(bt.v) if v is None else v, table.cuda(), bt.starts.cuda(),
             bt.lens.cuda()]
     q.qmv_paged_attention(qd, *keep, out, ls, bt.T, bt.Hq, bt.Hkv, bt.D, len(bt.new), bt.n_pages, bt.page,
-                          bt.max_pages, kw.pop("scale", 1.0 / math.sqrt(bt.D)), bt.dtype, slopes=sl,
+                          table.shape[1], kw.pop("scale", 1.0 / math.sqrt(bt.D)), bt.dtype, slopes=sl,
                           max_q_len=(max(bt.new) if bt.new else 0) if max_q_len is None else max_q_len, cache_strides=bt.strides,
                           q_strides=qs, workspace=workspace, softcap=kw.pop("cap", 0.0), stream=stream, **kw)
     torch.cuda.synchronize()

@@ -23,7 +23,8 @@ def ws(q):
 def both(q, ws, bt, **kw):
     ref = attention64(bt, **{k: v for k, v in kw.items() if k not in ("q_strided", "max_q_len")})
     for w in (ws, None):
-        check_attention(bt, *run_attention(q, bt, workspace=w, **kw), ref)
+        for wide in (False, True):
+            check_attention(bt, *run_attention(q, bt, workspace=w, wide=wide, **kw), ref)
 
 
 # new tokens, keys, Hq, Hkv, D, page
@@ -117,12 +118,12 @@ def test_lowest_and_infinite_scores(q, ws, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("new", [1, 3, 150])
-def test_bad_pages_make_their_rows_nan(q, ws, dtype, new):
+@pytest.mark.parametrize("new,wide", [(1, False), (3, False), (150, False), (150, True)])
+def test_bad_pages_make_their_rows_nan(q, ws, dtype, new, wide):
     bt = Batch([new, new], [200, 200], 4, 2, 128, 16, dtype)
     ref = attention64(bt)
     bt.table[0, 6] = bt.n_pages                                   # positions 96..111 of the first sequence
-    out, lse = run_attention(q, bt, workspace=ws)
+    out, lse = run_attention(q, bt, workspace=ws, wide=wide)
     sees = torch.arange(200 - new, 200) >= 96
     assert torch.isnan(out[:new].cpu()[sees]).all() and torch.isnan(lse[:new].cpu()[sees]).all()
     o, l, tol, tl = ref
@@ -131,7 +132,7 @@ def test_bad_pages_make_their_rows_nan(q, ws, dtype, new):
     # a window that ends behind the bad page does not see it
     kw = dict(window=60)
     ref = attention64(bt, **kw)
-    out, lse = run_attention(q, bt, workspace=ws, **kw)
+    out, lse = run_attention(q, bt, workspace=ws, wide=wide, **kw)
     keep = torch.cat([(torch.arange(200 - new, 200) < 96) | (torch.arange(200 - new, 200) - 60 >= 111),
                       torch.ones(new, dtype=torch.bool)])
     assert ((out.cpu().double() - ref[0]).abs() <= ref[2])[keep].all()
@@ -142,29 +143,29 @@ def test_bad_pages_make_their_rows_nan(q, ws, dtype, new):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("new", [1, 90])
-def test_strides_alignment_and_hints(q, ws, dtype, new):
+@pytest.mark.parametrize("new,wide", [(1, False), (90, False), (90, True)])
+def test_strides_alignment_and_hints(q, ws, dtype, new, wide):
     """Queries inside fused rows; a wrong or absent max_q_len; no lse; a cache
     that starts off a 16-byte boundary."""
     bt = Batch([new, 1], [150, 300], 8, 2, 64, 16, dtype)
     ref = attention64(bt)
     for hint in (0, 1, 1000):
-        check_attention(bt, *run_attention(q, bt, workspace=ws, max_q_len=hint, q_strided=True), ref)
-    check_attention(bt, *run_attention(q, bt, workspace=ws, lse=False), ref)
+        check_attention(bt, *run_attention(q, bt, workspace=ws, max_q_len=hint, q_strided=True, wide=wide), ref)
+    check_attention(bt, *run_attention(q, bt, workspace=ws, lse=False, wide=wide), ref)
 
     def shifted(t):
         b = bt.cache(t)
         big = torch.empty(b.numel() + 1, dtype=b.dtype, device="cuda")
         big[1:].copy_(b.reshape(-1))
         return big[1:]
-    check_attention(bt, *run_attention(q, bt, workspace=ws, k=shifted(bt.k), v=shifted(bt.v)), ref)
+    check_attention(bt, *run_attention(q, bt, workspace=ws, k=shifted(bt.k), v=shifted(bt.v), wide=wide), ref)
 
 
 def test_long_context_split_and_repeatable(q, ws):
     """One token over many keys: the split over blocks, the same twice, and the
     workspace left ready for a call of another size."""
-    for dtype in ("bf16", "f32"):
-        bt = Batch([1, 2], [9000, 3333], 8, 2, 128, 64, dtype, seed=3)
+    for dtype, new in (("bf16", [1, 2]), ("f32", [1, 2]), ("bf16", [70, 20]), ("f16", [300, 1])):
+        bt = Batch(new, [9000, 3333], 8, 2, 128, 64, dtype, seed=3)
         ref = attention64(bt)
         a = run_attention(q, bt, workspace=ws)
         check_attention(bt, *a, ref)

@@ -796,6 +796,7 @@ namespace qmv {
 int api_finish(cudaError_t e) { return finish(e); }
 int api_sms() { return device_sms(); }
 unsigned* api_fault_word() { return fault_word(); }
+int api_test_skip() { return g_test_skip.load(std::memory_order_relaxed); }
 bool api_encode_pages(CUtensorMap* m, const void* base, bool f16, int D, int page, int heads, int pages, long long tok_s,
                       long long head_s, long long page_s, int rows);
 }  // namespace qmv

@@ -116,7 +116,7 @@ struct Waiter {
 // into step.
 __device__ __forceinline__ bool warp_wait_all(Waiter& w, uint32_t bar, uint32_t parity) {
     const bool r = w(bar, parity);
-    w.ok = __all_sync(0xFFFFFFFFu, r) && w.ok;
+    w.ok = __all_sync(0xFFFFFFFFu, r && w.ok);      // one lane of a warp may have given up alone
     __syncwarp();
     return w.ok;
 }
@@ -449,7 +449,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
 #pragma unroll 1
                     for (; j < k1; j += 2) {
                         const uint32_t base = ring_a + slot * Gm::SLOT;
-                        if (__all_sync(0xFFFFFFFFu, pg >= 0)) {
+                        // test hook (qmv_test_skip_last_copy): block 0's first K tile never comes
+                        if (p.test_skip && blockIdx.x == 0 && w == 0 && fills == 0) {
+                            pg = -1;
+                        } else if (__all_sync(0xFFFFFFFFu, pg >= 0)) {
                             const int npg = page_of((j + 2) * kTile);
                             flush();
                             if (!warp_wait_all(wait, empty_a + slot * 8, sph)) break;

@@ -17,6 +17,7 @@ namespace qmv {
 int api_finish(cudaError_t e);      // QMV_OK, or QMV_ECUDA (recorded for qmv_last_cuda_error)
 int api_sms();                      // multiprocessors of the current device
 unsigned* api_fault_word();         // fault word of the current device, null if unknown
+int api_test_skip();                // whether qmv_test_skip_last_copy is on
 bool api_encode_pages(CUtensorMap* m, const void* base, bool f16, int D, int page, int heads, int pages, long long tok_s,
                       long long head_s, long long page_s, int rows);
 
@@ -65,6 +66,7 @@ struct AttnParams {
     unsigned* counters;             // workspace, null: no split over the keys
     float* partials;
     unsigned* fault;
+    int test_skip;                  // tests only (qmv_test_skip_last_copy)
 };
 
 constexpr float kLog2e = 1.4426950408889634f;

@@ -59,6 +59,21 @@ int check_cache(const qmv_paged_kv* kv) {
     return QMV_OK;
 }
 
+// Which kernel of the 16-bit types: 16 rows a kv head and unit, keys streamed by
+// warp, or 256 rows on the tensor cores.  Measured, heads of 128, 4 query heads
+// a kv head (us, few / many): 32 sequences of 4000 keys, 16 rows 90 / 137, 24
+// rows 175 / 138; one of 100000, 32 rows 141 / 164, 48 rows 200 / 167; one
+// of 2000, 96 rows 23 / 32.  So: up to 16 rows the first; up to 32 while its
+// units leave SMs free (it reads keys twice, from the second-level cache); and
+// any number while its tiles, by the longest sequence the table can hold, are
+// so few that a call's latency decides.
+bool many_rows(const qmv::AttnParams& p, int max_q_len) {
+    const double rows = (double)max_q_len * p.G, sms = qmv::api_sms();
+    const double units = (double)p.n_seqs * p.Hkv * ceil(rows / 16), tiles = (double)p.max_pages * p.page / 64;
+    if (rows <= 16 || (rows <= 32 && units <= 2 * sms)) return false;
+    return units * tiles > 24 * sms;
+}
+
 int check_cache_pointers(const qmv_paged_kv* kv) {
     if (!kv->k || !kv->v || !kv->page_table || !kv->q_starts || !kv->kv_lens) return QMV_EINVAL;
     const size_t eb = (size_t)elem_bytes(kv->dtype);
@@ -242,8 +257,9 @@ int qmv_paged_attention(const void* q, const qmv_paged_kv* kv, void* out, float*
     if (vec == 16 && near) {
         p.fault = qmv::api_fault_word();
         if (!p.fault) return QMV_ECUDA;
+        p.test_skip = qmv::api_test_skip();
         const int most = max_q_len > 0 && max_q_len < T ? max_q_len : T;
-        if ((long long)most * p.G > 16 && D <= 128) return qmv::api_finish(qmv::launch_attn_chunk(kv->dtype, p, s));
+        if (D <= 128 && many_rows(p, most)) return qmv::api_finish(qmv::launch_attn_chunk(kv->dtype, p, s));
         return qmv::api_finish(qmv::launch_attn_few(kv->dtype, p, most, s));
     }
     return qmv::api_finish(qmv::launch_attn_rows(kv->dtype, p, s));
