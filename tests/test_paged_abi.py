@@ -99,8 +99,20 @@ def test_attention_refusals():
     assert attention(ws=A + 8) == EALIGN and attention(out=B + 1) == EALIGN
     for bad in (dict(hq=0), dict(hq=3), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
                 dict(scale=float("inf")), dict(cap=-1.0), dict(cap=float("nan")), dict(cap=float("inf")),
-                dict(window=-1), dict(most=-1), dict(qs=(-1, 64)), dict(os=(255, 64)), dict(os=(256, 0))):
+                dict(scale=3e38), dict(scale=1.0, cap=1e-39), dict(window=-1), dict(most=-1), dict(qs=(-1, 64)), dict(os=(255, 64)), dict(os=(256, 0))):
         assert attention(**bad) == EINVAL, bad
+
+
+def test_too_many_rows():
+    assert attention(T=2 ** 28, hq=8, most=1) == EUNSUP
+
+
+def test_host_tensors_are_refused():
+    import torch
+    t = torch.zeros(4, 4, 64)
+    assert rope(x=t) == EINVAL and rope(y=t) == EINVAL
+    assert append(qkv=t) == EINVAL and append(k=t) == EINVAL
+    assert attention(q=t) == EINVAL and attention(out=t) == EINVAL
 
 
 def test_a_size_beyond_int_is_not_narrowed():

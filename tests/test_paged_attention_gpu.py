@@ -99,6 +99,18 @@ def test_what_a_row_does_not_see_never_reaches_it(q, ws, dtype, new):
         both(q, ws, bt, window=40)
 
 
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f16", 64)])
+def test_a_value_that_all_rows_see(q, ws, dtype, D):
+    """An infinite and a NaN value far back in a long context: every row of a
+    chunk is summed again exactly, in all its parts."""
+    bt = Batch([90, 40], [9000, 700], 4, 2, D, 16, dtype)
+    bt.vals[0][17, 0, 3], bt.vals[0][8000, 1, 5], bt.vals[1][650, :, 7] = float("inf"), float("nan"), -float("inf")
+    for b in range(2):
+        bt.store(b, bt.keys[b], bt.vals[b])
+    both(q, ws, bt)
+    both(q, ws, bt, window=500, cap=20.0)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 def test_lowest_and_infinite_scores(q, ws, dtype):
     """Scores of the type's lowest value, all scores -infinity (zeros), one
@@ -208,6 +220,37 @@ def test_captured_and_replayed_with_new_lengths(q, ws, dtype):
         part.q = bt.q
         part.keys, part.vals = ([t[:n] for t, n in zip(s, part.kv)] for s in (bt.keys, bt.vals))
         check_attention(part, out, lse, attention64(part))
+
+
+def test_first_call_of_a_process_may_be_captured():
+    """Nothing has to run before a capture."""
+    code = '''
+import torch, weight_quantized_matrix_b200 as q
+i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")
+for T, wide in ((1, 13), (200, 40000)):
+    qkv = torch.randn(T, 8 * 64, device="cuda").bfloat16()
+    k, v = (torch.zeros(20, 16, 2, 64, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    table = torch.zeros(1, wide, dtype=torch.int32, device="cuda")
+    table[0, :13] = torch.arange(13, device="cuda")
+    starts, lens, f = i32(0, T), i32(T), torch.ones(32, device="cuda")
+    qr, out = (torch.empty(T, 4, 64, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    ws = torch.zeros(q.PAGED_ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        q.qmv_kv_append(qkv, k, v, table, starts, lens, f, qr, T, 4, 2, 64, 64, "half", 1, 20, 16, wide, "bf16")
+        q.qmv_paged_attention(qr, k, v, table, starts, lens, out, None, T, 4, 2, 64, 1, 20, 16, wide, 0.125, "bf16", workspace=ws)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.isfinite(out.float()).all() and (out != 0).any()
+    if T == 1:
+        assert torch.equal(out[0].view(2, 2, 64), qkv[0, 6 * 64:].view(2, 1, 64).expand(2, 2, 64))   # one key: its value
+print("captured")
+'''
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 def test_two_streams_with_their_own_workspaces(q):

@@ -343,6 +343,18 @@ def qmv_rope_frequencies(rot_dim, base=10000.0, scaling="plain", factor=1.0, ori
     return list(buf), mag.value
 
 
+def _here(what, *tensors):
+    """The kernels run on the current device: tensors elsewhere are refused
+    (device addresses given as integers are taken as they are)."""
+    for t in tensors:
+        if t is not None and not isinstance(t, int):
+            if not t.is_cuda:
+                raise QmvError(-1, what + ": a tensor is not on a CUDA device")
+            import torch
+            if t.get_device() != torch._C._cuda_getDevice():
+                raise QmvError(-1, what + ": a tensor is not on the current device")
+
+
 def _layout(v):
     return v if isinstance(v, int) else ROPE_LAYOUTS[v]
 
@@ -353,6 +365,7 @@ def qmv_rope(x, y, positions, inv_freq, T, H, D, rot_dim, layout, dtype, magnitu
     rot_dim dims of every head turned by positions[t] * inv_freq; layout "half"
     or "interleaved"; strides are (token, head) in elements, dense if None;
     y may be x."""
+    _here("qmv_rope", x, y)
     xs = x_strides or (H * D, D)
     ys = y_strides or (H * D, D)
     st = _fast.rope(_ptr(x), _ptr(y), _ptr(positions), _ptr(inv_freq), T, H, D, rot_dim, _layout(layout),
@@ -369,6 +382,7 @@ def qmv_kv_append(qkv, k_cache, v_cache, page_table, q_starts, kv_lens, inv_freq
     paged cache.  cache_strides is (page, token, head) in elements, None for
     [n_pages, page_size, n_kv_heads, head_dim]; inv_freq None stores without a
     rotation, q_out None leaves the queries alone."""
+    _here("qmv_kv_append", qkv, k_cache, q_out)
     cs = cache_strides or (page_size * n_kv_heads * head_dim, n_kv_heads * head_dim, head_dim)
     st = _fast.kv_append(_ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(q_starts), _ptr(kv_lens), n_pages,
                          page_size, n_kv_heads, head_dim, _dtype(dtype), n_seqs, max_pages, cs[0], cs[1], cs[2],
@@ -389,6 +403,7 @@ def qmv_paged_attention(q, k_cache, v_cache, page_table, q_starts, kv_lens, out,
     out_strides are (token, head) in elements.  workspace: None, or a
     zero-filled device buffer of PAGED_ATTENTION_WORKSPACE_BYTES bytes that
     every call leaves ready for the next."""
+    _here("qmv_paged_attention", q, k_cache, out)
     cs = cache_strides or (page_size * n_kv_heads * head_dim, n_kv_heads * head_dim, head_dim)
     qs = q_strides or (n_q_heads * head_dim, head_dim)
     os_ = out_strides or (n_q_heads * head_dim, head_dim)

@@ -30,7 +30,7 @@
 // The weights are rounded to the element type for the second product, their
 // sum is not: an error of the size of the output's own rounding.
 //
-// Every wait is bounded (about one second); one that runs out ORs a code into
+// Every wait is bounded (about one second, not counting rows summed again); one that runs out ORs a code into
 // the fault word (1: softmax, 2: copies, 8: products, 16: scheduling), raises a flag that ends
 // every other wait, and the block frees its tensor memory and ends.
 #include <limits.h>
@@ -79,6 +79,7 @@ struct Bars {
     uint64_t pc_full[kPieces], pc_empty[kPieces];
     uint32_t tmem;
     volatile int abort;
+    int busy;                // warps that sum rows again: nobody gives up meanwhile
     int turn[4];             // taken while a warp of the scheduler's pair has its exponentials
 };
 
@@ -97,9 +98,10 @@ struct Waiter {
     bool ok;
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) {
         if (mbar_try_sleep(bar, parity)) return true;
-        const uint64_t t0 = now_ns();
+        uint64_t t0 = now_ns();
         while (ok) {
             if (mbar_try_sleep(bar, parity)) return true;
+            if (*(volatile int*)&b->busy) t0 = now_ns();
             if (b->abort || now_ns() - t0 > kWaitNs) {
                 if (!b->abort && fault) atomicOr(fault, code);
                 b->abort = 1;
@@ -145,35 +147,53 @@ template <class T, int DP, bool MOD>
 __device__ __forceinline__ void exact_row(const AttnParams& p, const ScoreMod<false>& mod, int b, int hk, const T* q, int pos,
                                           int k0, int k1, float slope, float (&o)[DP / 32], float& m, float& l) {
     const int lane = threadIdx.x & 31;
-    float qv[DP / 32];
 #pragma unroll
-    for (int i = 0; i < DP / 32; ++i) {
-        const int d = lane + 32 * i;
-        qv[i] = d < p.D ? ld_elem(q + d) : 0.0f;
-        o[i] = 0.0f;
-    }
+    for (int i = 0; i < DP / 32; ++i) o[i] = 0.0f;
     m = -INFINITY;
     l = 0.0f;
 #pragma unroll 1
-    for (int j = k0; j < k1; ++j) {
-        const long long at = key_place(p, b, hk, j);
+    for (int j0 = k0; j0 < k1; j0 += 32) {
+        // 32 scores, a key a lane
+        const bool in = j0 + lane < k1;
+        const long long at = in ? key_place(p, b, hk, j0 + lane) : -1;
         float s = 0.0f;
+#pragma unroll 2
+        for (int c = 0; c < p.D && at >= 0; c += 8) {
+            const uint4 kq = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.k) + at + c));
+            const uint4 qq = __ldg(reinterpret_cast<const uint4*>(q + c));
+            const uint32_t kw[4] = {kq.x, kq.y, kq.z, kq.w}, qw[4] = {qq.x, qq.y, qq.z, qq.w};
 #pragma unroll
-        for (int i = 0; i < DP / 32; ++i) {
-            const int d = lane + 32 * i;
-            if (at >= 0 && d < p.D) s = fmaf(qv[i], ld_elem(static_cast<const T*>(p.k) + at + d), s);
+            for (int e = 0; e < 4; ++e) {
+                const float2 a = unpack2<T>(kw[e]), x = unpack2<T>(qw[e]);
+                s = fmaf(a.x, x.x, s);
+                s = fmaf(a.y, x.y, s);
+            }
         }
+        s = MOD ? mod.apply(s, slope, j0 + lane - pos) : s * p.scale * kLog2e;
+        s = !in ? -INFINITY : at < 0 ? NAN : s;
+        float mn = s;
 #pragma unroll
-        for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, w);
-        s = at < 0 ? NAN : MOD ? mod.apply(s, slope, j - pos) : s * p.scale * kLog2e;
-        const float mn = fmaxf(m, s), base = mn == -INFINITY ? 0.0f : mn, f = ex2(m - base), w = ex2(s - base);
-        l = fmaf(l, f, w);
+        for (int w = 16; w > 0; w >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, w));
+        mn = fmaxf(m, mn);
+        const float base = mn == -INFINITY ? 0.0f : mn, f = ex2(m - base), w = in ? ex2(s - base) : 0.0f;
         m = mn;
+        float sum = w;
 #pragma unroll
-        for (int i = 0; i < DP / 32; ++i) {
-            const int d = lane + 32 * i;
-            o[i] = at >= 0 && d < p.D ? fmaf(w, ld_elem(static_cast<const T*>(p.v) + at + d), o[i] * f) : o[i] * f;
-            if (at < 0) o[i] = NAN;
+        for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+        l = fmaf(l, f, sum);
+#pragma unroll
+        for (int i = 0; i < DP / 32; ++i) o[i] *= f;
+#pragma unroll 4
+        for (int x = 0; x < 32; ++x) {
+            const float wx = __shfl_sync(0xFFFFFFFFu, w, x);
+            const long long ax = __shfl_sync(0xFFFFFFFFu, at, x);
+            if (j0 + x >= k1) continue;
+#pragma unroll
+            for (int i = 0; i < DP / 32; ++i) {
+                const int d = lane + 32 * i;
+                if (ax < 0) o[i] = NAN;
+                else if (d < p.D) o[i] = fmaf(wx, ld_elem(static_cast<const T*>(p.v) + ax + d), o[i]);
+            }
         }
     }
 }
@@ -207,6 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         for (int i = 0; i < kPieces; ++i) { mbar_init1(&bars.pc_full[i], 1); mbar_init1(&bars.pc_empty[i], kReaders); }
         for (int i = 0; i < 4; ++i) bars.turn[i] = 0;
         bars.abort = 0;
+        bars.busy = 0;
         fence_mbar_init();
     }
     __syncwarp();
@@ -266,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                                 rows_keys(p, sc.s, r0, r1, lo, hi);
                                 if (lo < hi) {
                                     a = max(k0, lo / kTile);
-                                    e = min(k1, (hi + kTile - 1) / kTile);
+                                    e = min(k1, (hi - 1) / kTile + 1);
                                     if (a >= e) a = e = k0;
                                 }
                             }
@@ -661,6 +682,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                 p.lse[row * p.Hq + head] = empty ? -INFINITY : (m + log2f(l)) * kLn2;
             }
             unsigned again = __ballot_sync(0xFFFFFFFFu, mine && any && odd && !empty);
+            if (again && lane == 0) atomicAdd(&bars.busy, 1);      // may take long; it waits for nothing
+            const bool busy = again != 0;
 #pragma unroll 1
             while (again) {
                 const int src = __ffs(again) - 1;
@@ -688,6 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                     p.lse[srow * p.Hq + shead] = sl == 0.0f ? -INFINITY : (sm2 + log2f(sl)) * kLn2;
                 }
             }
+            if (busy && lane == 0) atomicAdd(&bars.busy, -1);
             if (part && nrows > (r & ~31)) {             // this warp has rows
                 // A warp joins its own rows: the last of the unit's blocks to
                 // have written them does.

@@ -59,7 +59,7 @@ __device__ __forceinline__ int unit_tiles(const AttnParams& p, const SeqInfo& s,
     int lo, hi;
     rows_keys(p, s, i * ROWS, min((i + 1) * ROWS, s.n * p.G) - 1, lo, hi);
     first = lo / TK;
-    return (hi + TK - 1) / TK - first;
+    return hi > lo ? (hi - 1) / TK + 1 - first : 0;
 }
 
 constexpr int kAlignTiles = 64;         // parts up to this many tiles end with their units

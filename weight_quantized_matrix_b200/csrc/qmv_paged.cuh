@@ -93,7 +93,7 @@ __device__ __forceinline__ int seq_of_row(const int* q_starts, int n_seqs, int t
 // Keys [lo, hi) that the token at position pos of a sequence of len keys sees.
 __device__ __forceinline__ void visible_keys(const AttnParams& p, int pos, int len, int& lo, int& hi) {
     hi = p.causal ? min(len, pos + 1) : len;
-    lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+    lo = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
     if (hi < 0) hi = 0;
 }
 

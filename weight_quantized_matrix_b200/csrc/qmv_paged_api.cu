@@ -216,7 +216,8 @@ int qmv_paged_attention(const void* q, const qmv_paged_kv* kv, void* out, float*
     if (T < 0 || n_q_heads < 1 || n_q_heads % kv->n_kv_heads != 0 || max_q_len < 0) return QMV_EINVAL;
     if ((long long)T * n_q_heads > 0x7FFFFFFF) return QMV_EUNSUPPORTED;
     if (causal != 0 && causal != 1) return QMV_EINVAL;
-    if (window < 0 || !(softcap >= 0.0f) || isinf(softcap) || !(scale > 0.0f) || isinf(scale)) return QMV_EINVAL;
+    if (window < 0 || !(softcap >= 0.0f) || isinf(softcap) || !(scale > 0.0f) || isinf(scale * qmv::kLog2e)) return QMV_EINVAL;
+    if (softcap > 0.0f && isinf(scale / softcap * (2.0f * qmv::kLog2e))) return QMV_EINVAL;
     const int D = kv->head_dim;
     const long long size[2] = {T, n_q_heads}, os[2] = {out_token_stride, out_head_stride};
     if (q_token_stride < 0 || q_head_stride < 0 || !disjoint(D, 2, size, os)) return QMV_EINVAL;
@@ -238,7 +239,7 @@ int qmv_paged_attention(const void* q, const qmv_paged_kv* kv, void* out, float*
     // exact for r G < 2^32 (G > 1; r < T G)
     if (p.G > 1 && (long long)T * p.G * p.G < (1LL << 32)) p.g_mul = (unsigned)((1ULL << 32) / p.G + 1);
     p.causal = causal;
-    p.window = window > (1 << 30) ? 0 : window;      // wider than any position: none
+    p.window = window;
     p.scale = scale; p.softcap = softcap;
     if (workspace) {
         p.counters = static_cast<unsigned*>(workspace);
