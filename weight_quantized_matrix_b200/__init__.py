@@ -343,16 +343,25 @@ def qmv_rope_frequencies(rot_dim, base=10000.0, scaling="plain", factor=1.0, ori
     return list(buf), mag.value
 
 
-def _here(what, *tensors):
-    """The kernels run on the current device: tensors elsewhere are refused
-    (device addresses given as integers are taken as they are)."""
-    for t in tensors:
-        if t is not None and not isinstance(t, int):
-            if not t.is_cuda:
-                raise QmvError(-1, what + ": a tensor is not on a CUDA device")
-            import torch
-            if t.get_device() != torch._C._cuda_getDevice():
-                raise QmvError(-1, what + ": a tensor is not on the current device")
+_current = None
+
+
+def _stream_device(s):
+    """Raw stream and current device (-1 where CUDA is not in use).  The kernels
+    run on the current device; arrays given as tensors have to be there."""
+    global _current
+    if _current is None:
+        import torch
+        if s is not None and not torch.cuda.is_initialized():
+            return _stream(s), -1
+        c = torch._C
+        _current = c._cuda_getDevice, getattr(c, "_cuda_getCurrentRawStream", None)
+        if s is None:
+            torch.cuda.current_stream()          # initializes CUDA
+    dev = _current[0]()
+    if s is None:
+        return (_current[1](dev) if _current[1] else _stream(None)), dev
+    return _stream(s), dev
 
 
 def _layout(v):
@@ -365,11 +374,10 @@ def qmv_rope(x, y, positions, inv_freq, T, H, D, rot_dim, layout, dtype, magnitu
     rot_dim dims of every head turned by positions[t] * inv_freq; layout "half"
     or "interleaved"; strides are (token, head) in elements, dense if None;
     y may be x."""
-    _here("qmv_rope", x, y)
     xs = x_strides or (H * D, D)
     ys = y_strides or (H * D, D)
-    st = _fast.rope(_ptr(x), _ptr(y), _ptr(positions), _ptr(inv_freq), T, H, D, rot_dim, _layout(layout),
-                    _dtype(dtype), xs[0], xs[1], ys[0], ys[1], magnitude, _stream(stream))
+    st = _fast.rope(x, y, positions, inv_freq, T, H, D, rot_dim, _layout(layout), _dtype(dtype), xs[0], xs[1], ys[0],
+                    ys[1], magnitude, *_stream_device(stream))
     if st:
         raise QmvError(st, "qmv_rope")
 
@@ -382,13 +390,13 @@ def qmv_kv_append(qkv, k_cache, v_cache, page_table, q_starts, kv_lens, inv_freq
     paged cache.  cache_strides is (page, token, head) in elements, None for
     [n_pages, page_size, n_kv_heads, head_dim]; inv_freq None stores without a
     rotation, q_out None leaves the queries alone."""
-    _here("qmv_kv_append", qkv, k_cache, q_out)
     cs = cache_strides or (page_size * n_kv_heads * head_dim, n_kv_heads * head_dim, head_dim)
-    st = _fast.kv_append(_ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(q_starts), _ptr(kv_lens), n_pages,
-                         page_size, n_kv_heads, head_dim, _dtype(dtype), n_seqs, max_pages, cs[0], cs[1], cs[2],
-                         _ptr(qkv), _ptr(positions), _ptr(inv_freq), _ptr(q_out), T, n_q_heads, rot_dim,
-                         _layout(layout), (n_q_heads + 2 * n_kv_heads) * head_dim if qkv_stride is None else qkv_stride,
-                         n_q_heads * head_dim if q_out_stride is None else q_out_stride, magnitude, _stream(stream))
+    st = _fast.kv_append(k_cache, v_cache, page_table, q_starts, kv_lens, n_pages, page_size, n_kv_heads, head_dim,
+                         _dtype(dtype), n_seqs, max_pages, cs[0], cs[1], cs[2], qkv, positions, inv_freq, q_out, T,
+                         n_q_heads, rot_dim, _layout(layout),
+                         (n_q_heads + 2 * n_kv_heads) * head_dim if qkv_stride is None else qkv_stride,
+                         n_q_heads * head_dim if q_out_stride is None else q_out_stride, magnitude,
+                         *_stream_device(stream))
     if st:
         raise QmvError(st, "qmv_kv_append")
 
@@ -403,15 +411,13 @@ def qmv_paged_attention(q, k_cache, v_cache, page_table, q_starts, kv_lens, out,
     out_strides are (token, head) in elements.  workspace: None, or a
     zero-filled device buffer of PAGED_ATTENTION_WORKSPACE_BYTES bytes that
     every call leaves ready for the next."""
-    _here("qmv_paged_attention", q, k_cache, out)
     cs = cache_strides or (page_size * n_kv_heads * head_dim, n_kv_heads * head_dim, head_dim)
     qs = q_strides or (n_q_heads * head_dim, head_dim)
     os_ = out_strides or (n_q_heads * head_dim, head_dim)
-    st = _fast.paged_attention(_ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(q_starts), _ptr(kv_lens), n_pages,
-                               page_size, n_kv_heads, head_dim, _dtype(dtype), n_seqs, max_pages, cs[0], cs[1], cs[2],
-                               _ptr(q), _ptr(out), _ptr(lse), _ptr(slopes), _ptr(workspace), T, n_q_heads,
-                               int(bool(causal)), window, max_q_len, qs[0], qs[1], os_[0], os_[1], scale, softcap,
-                               _stream(stream))
+    st = _fast.paged_attention(k_cache, v_cache, page_table, q_starts, kv_lens, n_pages, page_size, n_kv_heads,
+                               head_dim, _dtype(dtype), n_seqs, max_pages, cs[0], cs[1], cs[2], q, out, lse, slopes,
+                               workspace, T, n_q_heads, 1 if causal else 0, window, max_q_len, qs[0], qs[1], os_[0],
+                               os_[1], scale, softcap, *_stream_device(stream))
     if st:
         raise QmvError(st, "qmv_paged_attention")
 

@@ -44,6 +44,26 @@ static int as_float(PyObject* o, float* out) {
     return 0;
 }
 
+/* An array argument of the calls below: None, an int (a device address), or a
+ * tensor, of which data_ptr() is taken.  A tensor that is not on device `dev` (-1:
+ * not known) or not on a CUDA device at all sets *elsewhere. */
+static PyObject *s_data_ptr, *s_get_device;
+static int as_array(PyObject* o, int dev, void** out, int* elsewhere) {
+    if (o == Py_None || PyLong_Check(o)) return as_ptr(o, out);
+    PyObject* r = PyObject_CallMethodNoArgs(o, s_data_ptr);
+    if (!r) return -1;
+    *out = PyLong_AsVoidPtr(r);
+    Py_DECREF(r);
+    if (*out == NULL && PyErr_Occurred()) return -1;
+    r = PyObject_CallMethodNoArgs(o, s_get_device);
+    if (!r) return -1;
+    const long d = PyLong_AsLong(r);
+    Py_DECREF(r);
+    if (d == -1 && PyErr_Occurred()) return -1;
+    if (d < 0 || (dev >= 0 && d != dev)) *elsewhere = 1;
+    return 0;
+}
+
 /* affine(x, w, scales, biases, y, M, N, K, bits, group, dtype, batch, x_batched, stream) -> status */
 static PyObject* py_affine(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     (void)self;
@@ -96,19 +116,21 @@ static PyObject* py_block_scaled(PyObject* self, PyObject* const* a, Py_ssize_t 
     return PyLong_FromLong(r);
 }
 
-/* rope(x, y, positions, inv_freq, T, H, D, rot, layout, dtype, xt, xh, yt, yh, magnitude, stream) -> status */
+/* rope(x, y, positions, inv_freq, T, H, D, rot, layout, dtype, xt, xh, yt, yh, magnitude, stream, device) -> status */
 static PyObject* py_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     (void)self;
-    if (n != 16) { PyErr_SetString(PyExc_TypeError, "rope() takes 16 arguments"); return NULL; }
+    if (n != 17) { PyErr_SetString(PyExc_TypeError, "rope() takes 17 arguments"); return NULL; }
     void* p[4];
-    int v[6];
+    int v[6], dev, elsewhere = 0;
     long long s[4];
     float mag;
     void* st;
-    for (int i = 0; i < 4; ++i) if (as_ptr(a[i], &p[i])) return NULL;
+    if (as_int(a[16], &dev)) return NULL;
+    for (int i = 0; i < 4; ++i) if (as_array(a[i], dev, &p[i], &elsewhere)) return NULL;
     for (int i = 0; i < 6; ++i) if (as_int(a[4 + i], &v[i])) return NULL;
     for (int i = 0; i < 4; ++i) if (as_ll(a[10 + i], &s[i])) return NULL;
     if (as_float(a[14], &mag) || as_ptr(a[15], &st)) return NULL;
+    if (elsewhere) return PyLong_FromLong(QMV_EINVAL);
     int r;
     Py_BEGIN_ALLOW_THREADS
     r = qmv_rope(p[0], p[1], (const int*)p[2], (const float*)p[3], v[0], v[1], v[2], v[3], v[4], mag, s[0], s[1], s[2],
@@ -120,11 +142,11 @@ static PyObject* py_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 /* The 15 leading arguments of the two calls on a paged cache: k, v,
  * page_table, q_starts, kv_lens, n_pages, page_size, n_kv_heads, head_dim,
  * dtype, n_seqs, max_pages, page_stride, token_stride, head_stride. */
-static int as_cache(PyObject* const* a, qmv_paged_kv* kv) {
+static int as_cache(PyObject* const* a, int dev, qmv_paged_kv* kv, int* elsewhere) {
     void* p[5];
     int v[7];
     long long s[3];
-    for (int i = 0; i < 5; ++i) if (as_ptr(a[i], &p[i])) return -1;
+    for (int i = 0; i < 5; ++i) if (as_array(a[i], dev, &p[i], elsewhere)) return -1;
     for (int i = 0; i < 7; ++i) if (as_int(a[5 + i], &v[i])) return -1;
     for (int i = 0; i < 3; ++i) if (as_ll(a[12 + i], &s[i])) return -1;
     kv->k = p[0]; kv->v = p[1];
@@ -136,21 +158,22 @@ static int as_cache(PyObject* const* a, qmv_paged_kv* kv) {
 }
 
 /* kv_append(<cache>, qkv, positions, inv_freq, q_out, T, n_q_heads, rot, layout, qkv_stride, q_out_stride,
- * magnitude, stream) -> status */
+ * magnitude, stream, device) -> status */
 static PyObject* py_kv_append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     (void)self;
-    if (n != 27) { PyErr_SetString(PyExc_TypeError, "kv_append() takes 27 arguments"); return NULL; }
+    if (n != 28) { PyErr_SetString(PyExc_TypeError, "kv_append() takes 28 arguments"); return NULL; }
     qmv_paged_kv kv;
     void* p[4];
-    int v[4];
+    int v[4], dev, elsewhere = 0;
     long long s[2];
     float mag;
     void* st;
-    if (as_cache(a, &kv)) return NULL;
-    for (int i = 0; i < 4; ++i) if (as_ptr(a[15 + i], &p[i])) return NULL;
+    if (as_int(a[27], &dev) || as_cache(a, dev, &kv, &elsewhere)) return NULL;
+    for (int i = 0; i < 4; ++i) if (as_array(a[15 + i], dev, &p[i], &elsewhere)) return NULL;
     for (int i = 0; i < 4; ++i) if (as_int(a[19 + i], &v[i])) return NULL;
     for (int i = 0; i < 2; ++i) if (as_ll(a[23 + i], &s[i])) return NULL;
     if (as_float(a[25], &mag) || as_ptr(a[26], &st)) return NULL;
+    if (elsewhere) return PyLong_FromLong(QMV_EINVAL);
     int r;
     Py_BEGIN_ALLOW_THREADS
     r = qmv_kv_append(p[0], s[0], &kv, (const int*)p[1], (const float*)p[2], p[3], s[1], v[0], v[1], v[2], v[3], mag,
@@ -160,22 +183,23 @@ static PyObject* py_kv_append(PyObject* self, PyObject* const* a, Py_ssize_t n) 
 }
 
 /* paged_attention(<cache>, q, out, lse, slopes, workspace, T, n_q_heads, causal, window, max_q_len, q_ts, q_hs,
- * out_ts, out_hs, scale, softcap, stream) -> status */
+ * out_ts, out_hs, scale, softcap, stream, device) -> status */
 static PyObject* py_paged_attention(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     (void)self;
-    if (n != 32) { PyErr_SetString(PyExc_TypeError, "paged_attention() takes 32 arguments"); return NULL; }
+    if (n != 33) { PyErr_SetString(PyExc_TypeError, "paged_attention() takes 33 arguments"); return NULL; }
     qmv_paged_kv kv;
     void* p[5];
-    int v[5];
+    int v[5], dev, elsewhere = 0;
     long long s[4];
     float f[2];
     void* st;
-    if (as_cache(a, &kv)) return NULL;
-    for (int i = 0; i < 5; ++i) if (as_ptr(a[15 + i], &p[i])) return NULL;
+    if (as_int(a[32], &dev) || as_cache(a, dev, &kv, &elsewhere)) return NULL;
+    for (int i = 0; i < 5; ++i) if (as_array(a[15 + i], dev, &p[i], &elsewhere)) return NULL;
     for (int i = 0; i < 5; ++i) if (as_int(a[20 + i], &v[i])) return NULL;
     for (int i = 0; i < 4; ++i) if (as_ll(a[25 + i], &s[i])) return NULL;
     for (int i = 0; i < 2; ++i) if (as_float(a[29 + i], &f[i])) return NULL;
     if (as_ptr(a[31], &st)) return NULL;
+    if (elsewhere) return PyLong_FromLong(QMV_EINVAL);
     int r;
     Py_BEGIN_ALLOW_THREADS
     r = qmv_paged_attention(p[0], &kv, p[1], (float*)p[2], v[0], v[1], f[0], v[2], v[3], f[1], (const float*)p[3],
@@ -196,4 +220,9 @@ static PyMethodDef methods[] = {
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_qmv_fast", NULL, -1, methods};
 
-PyMODINIT_FUNC PyInit__qmv_fast(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__qmv_fast(void) {
+    s_data_ptr = PyUnicode_InternFromString("data_ptr");
+    s_get_device = PyUnicode_InternFromString("get_device");
+    if (!s_data_ptr || !s_get_device) return NULL;
+    return PyModule_Create(&module);
+}
