@@ -31,7 +31,7 @@ def check(y, x, pos, f, rot, layout, dtype, m):
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 @pytest.mark.parametrize("T,H,D,rot", [(1, 1, 64, 64), (1, 40, 128, 128), (7, 3, 80, 40), (33, 5, 96, 2), (3, 2, 2, 2),
-                                       (130, 1, 128, 64), (257, 12, 256, 256), (5, 7, 33, 10), (64, 1, 8, 6),
+                                       (130, 1, 128, 64), (257, 11, 256, 256), (5, 7, 33, 10), (64, 1, 8, 6),
                                        (19, 70, 100, 50)])
 def test_matches_definition(q, dtype, layout, T, H, D, rot):
     g = torch.Generator().manual_seed(T * 1000 + D)

@@ -57,7 +57,7 @@ __device__ __forceinline__ void f32_step(const unsigned char* kb, const unsigned
     float x[R], mx[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) x[r] = 0.0f;
-#pragma unroll 2
+#pragma unroll 4
     for (int c = 0; c < CPR / 2; ++c) {
         const float4 kv = *reinterpret_cast<const float4*>(kb + key * ROWB + (((hf * (CPR / 2) + c) ^ (key & 7)) << 4));
 #pragma unroll
@@ -111,7 +111,7 @@ __device__ __forceinline__ void f32_step(const unsigned char* kb, const unsigned
         if (hf == 0) s_p[r][key] = e;
     }
     __syncwarp();
-#pragma unroll 1
+#pragma unroll 2
     for (int k4 = 0; k4 < 16; k4 += 4) {
         float v[4][VEC];
 #pragma unroll
@@ -203,6 +203,18 @@ attn_f32_kernel(const __grid_constant__ AttnParams p, int page_shift) {
         auto issue = [&](int t, int slot, int at) {
             if (t < k1) {
                 const uint32_t base = mine_a + slot * Gm::STEP;
+                if (chunks == CPR && __all_sync(0xFFFFFFFFu, at >= 0)) {
+#pragma unroll 8
+                    for (int u = 0; u < 16 * CPR / 32; ++u) {
+                        const int id = u * 32 + lane, r = id / CPR, c = id % CPR;
+                        const long long off = (long long)__shfl_sync(0xFFFFFFFFu, at, r) * 16 + c * 16;
+                        const uint32_t d = base + r * ROWB + ((c ^ (r & 7)) << 4);
+                        cp16(d, kh + off);
+                        cp16(d + 16 * ROWB, vh + off);
+                    }
+                    cp_commit();
+                    return;
+                }
 #pragma unroll 8
                 for (int u = 0; u < 16 * CPR / 32; ++u) {
                     const int id = u * 32 + lane, r = id / CPR, c = id % CPR;
