@@ -12,9 +12,10 @@
 //
 // A block that ends one unit and begins another pays two joins, of about ten
 // tiles' time each.  Few tiles a block are therefore cut at the units' own ends
-// (every unit into parts of Q tiles, the last one shorter), as long as some Q up to
-// twice the even share gives no more parts than blocks; failing that, in
-// quarters of the even share, so that short units stay whole.
+// (every unit into parts of Q tiles, the last one shorter), if that gives no more
+// parts than blocks at the even share or 5/4 of it; failing that, in eighths of
+// the even share (at least 4 tiles), so that short units stay whole.  (Parts of up
+// to twice the share: 12 fp32 sequences of 100-2100 keys 56 us, so 48.)
 //
 // A block whose part ends or begins inside a unit leaves that unit's partial
 // result (unnormalised sums, maxima, weights) in the workspace and counts
@@ -160,7 +161,7 @@ template <int ROWS, int TK> struct Sched {
         split = p.partials != nullptr;
         live = false;
         Q = 1;
-        int v = 0, pass = 0;    // 0: count tiles, 1..4: parts of each, 5/4, 3/2, 2 times each tiles end with their units, 5: they do not
+        int v = 0, pass = 0;    // 0: count tiles, 1, 2: parts of each, 5/4 each tiles end with their units, 3: they do not
         int each = 0;           // tiles a block
         long long incl = 0, all;
 #pragma unroll 1
@@ -177,7 +178,7 @@ template <int ROWS, int TK> struct Sched {
                 if (all == 0) return;
                 if (all >> 30) {
                     Q = (int)(all >> 29) + 1;
-                    pass = 5;
+                    pass = 3;
                     continue;
                 }
                 each = (int)(((unsigned)all + gridDim.x - 1) / gridDim.x);
@@ -186,15 +187,15 @@ template <int ROWS, int TK> struct Sched {
                     pass = 1;
                     continue;
                 }
-            } else if (pass < 5 && all > (long long)gridDim.x) {
+            } else if (pass < 3 && all > (long long)gridDim.x) {
                 ++pass;
-                Q = pass == 5 ? max(4, each / 4) : max(min_tiles, each * (pass == 4 ? 8 : pass + 3) / 4);
+                Q = pass == 3 ? max(4, each / 8) : max(min_tiles, each * 5 / 4);
                 continue;
             }
             break;
         }
         W = (int)all;
-        nblk = pass >= 1 && pass < 5 ? W : min((int)gridDim.x, W);
+        nblk = pass == 1 || pass == 2 ? W : min((int)gridDim.x, W);
         if ((int)blockIdx.x >= nblk) return;
         q = W / nblk;
         rem = W - q * nblk;
