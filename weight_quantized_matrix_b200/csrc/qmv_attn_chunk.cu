@@ -20,8 +20,6 @@
 //              go by cp.async, 16 bytes at a time, with zeros for keys no row
 //              sees.  Q goes by cp.async.
 //   warp 10    hands the block's units out, one after the other.
-// A unit of up to 128 rows goes to both halves, which take its key tiles in turn:
-// such a unit is bound by the keys, and one half alone needs 2200 clocks a tile.
 // Tensor memory: S_0, S_1 (64 columns each), 2 x P_0, 2 x P_1 (32 each), O_0, O_1.
 // K and V tiles of 64 keys alternate in a ring.
 //
@@ -69,7 +67,6 @@ struct Piece {
     int k0, k1;              // key tiles
     int ulo, uhi;            // keys that any row sees
     int a[2], e[2];          // key tiles of each half
-    int both;                // up to 128 rows: both halves take them, tiles in turn
     int shared;              // other blocks have parts of the unit
     int slot;                // this block's partial result
     int c0, c1, slot0;       // first and last block of the unit; the first one's partial result
@@ -80,7 +77,6 @@ constexpr int kReaders = 2 + kLoaders + 8;   // warps that read a piece
 struct Bars {
     uint64_t kv_full[16], kv_empty[16], q_full, q_empty, s_full[2], s_empty[2], p_full[2][2], pv_done[2][2], drain[2];
     uint64_t pc_full[kPieces], pc_empty[kPieces];
-    uint64_t both_full[4], both_empty[4];        // half 1's result of shared rows, per 32 rows
     uint32_t tmem;
     volatile int abort;
     int busy;                // warps that sum rows again: nobody gives up meanwhile
@@ -229,11 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
             mbar_init1(&bars.drain[i], 1);
         }
         for (int i = 0; i < kPieces; ++i) { mbar_init1(&bars.pc_full[i], 1); mbar_init1(&bars.pc_empty[i], kReaders); }
-        for (int i = 0; i < 4; ++i) {
-            bars.turn[i] = 0;
-            mbar_init1(&bars.both_full[i], 1);
-            mbar_init1(&bars.both_empty[i], 1);
-        }
+        for (int i = 0; i < 4; ++i) bars.turn[i] = 0;
         bars.abort = 0;
         bars.busy = 0;
         fence_mbar_init();
@@ -286,10 +278,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                         pc.b = sc.b; pc.h = sc.h; pc.rbase = rbase;
                         pc.k0 = k0; pc.k1 = k1;
                         rows_keys(p, sc.s, rbase, min(rbase + kRows, rows) - 1, pc.ulo, pc.uhi);
-                        pc.both = rows - rbase <= kHalf;
 #pragma unroll 1
                         for (int h = 0; h < 2; ++h) {
-                            const int r0 = rbase + (pc.both ? 0 : h * kHalf), r1 = min(r0 + kHalf, rows) - 1;
+                            const int r0 = rbase + h * kHalf, r1 = min(r0 + kHalf, rows) - 1;
                             int a = k0, e = k0;
                             if (r0 <= r1) {
                                 int lo, hi;
@@ -360,9 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
             };
 #pragma unroll 1
             while (const Piece* pc = take(wait)) {
-                const int k0 = pc->k0, k1 = pc->k1, a = pc->a[h], e = pc->e[h], both = pc->both;
-                auto own = [&](int j) { return a <= j && j < e && !(both && ((j - k0) & 1) != h); };
-                bool fresh = true;                  // no second product of the unit yet
+                const int k0 = pc->k0, k1 = pc->k1, a = pc->a[h], e = pc->e[h];
                 if (one && k0 < k1) {
                     wait(s_addr(&bars.q_full), qph);
                     qph ^= 1u;
@@ -370,24 +359,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
 #pragma unroll 1
                     for (int j = k0 - 1; j < k1 && wait.ok; ++j) {
                         if (j + 1 < k1) {
-                            qk(own(j + 1));
+                            qk(a <= j + 1 && j + 1 < e);
                             if (j + 2 == k1) commit(qe_a);
                         }
                         if (j < k0) continue;
                         wait(full_a + vs * 8, vph);
-                        if (own(j)) {
+                        if (a <= j && j < e) {
                             const int u = pn & 1;
                             wait(pf_a + u * 8, (uint32_t)(pn >> 1) & 1u);
                             tc_after();
                             if (wait.ok) {
                                 const uint32_t v = (ring_d + vs * (Gm::SLOT / 16)) | LBO_V, w = tp + u * 32;
-                                mma_ts(to, w, v, HI, ID_O, !fresh);
+                                mma_ts(to, w, v, HI, ID_O, j > a);
 #pragma unroll
                                 for (int k = 1; k < kTile / 16; ++k)
                                     mma_ts(to, w + k * 8, v + k * (16 * 128 / 16), HI, ID_O, true);
                                 commit(pv_a + u * 8);
                             }
-                            fresh = false;
                             ++pn;
                         }
                         if (wait.ok) commit(empty_a + vs * 8);
@@ -460,14 +448,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                     if (npiece > 0 && !warp_wait_all(wait, s_addr(&bars.q_empty), (uint32_t)(npiece - 1) & 1u)) break;
 #pragma unroll 1
                     for (int gr = w; gr < kRows / 8; gr += kLoaders) {
-                        const int r = gr * 8 + (lane & 7), ur = pc->both ? r % kHalf : r;
-                        const int pr = rbase + min(ur, nrows - 1), ti = token_of(p, pr);
+                        const int r = gr * 8 + (lane & 7), pr = rbase + min(r, nrows - 1), ti = token_of(p, pr);
                         const long long off = ((long long)(pc->t0 + ti) * p.q_ts + (long long)(hk * p.G + pr - ti * p.G) * p.q_hs) * 2;
 #pragma unroll
                         for (int u = 0; u < PER; ++u) {
                             const int id = u * 32 + lane, rr = id / CPR, c = id % CPR, row = gr * 8 + rr;
                             const long long o = __shfl_sync(0xFFFFFFFFu, off, rr);
-                            const bool rd = (pc->both ? row % kHalf : row) < nrows && c < chunks;
+                            const bool rd = row < nrows && c < chunks;
                             const uint32_t d = q_a + (row / kHalf) * Gm::QB + (c / 8) * (128 * 128) + (row % kHalf) * 128 +
                                                (((c & 7) ^ (row & 7)) << 4);
                             cp16_or_zero(d, static_cast<const char*>(p.q) + (rd ? o + c * 16 : 0), rd);
@@ -556,11 +543,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
         const float scale2 = p.scale * kLog2e;
         Waiter wait{&bars, p.fault, 1u, true};
         int ns = 0;                                      // steps of this half so far
-        int nb = 0;                                      // units with shared rows so far
 #pragma unroll 1
         while (const Piece* pc = take(wait)) {
-            const int a = pc->a[h], e = pc->e[h], both = pc->both;
-            const int rbase = pc->rbase + (both ? 0 : h * kHalf), nrows = min(kHalf, pc->n * p.G - rbase);
+            const int a = pc->a[h], e = pc->e[h];
+            const int rbase = pc->rbase + h * kHalf, nrows = min(kHalf, pc->n * p.G - rbase);
             int lo = 0, hi = 0, pos = 0, ti = 0, head = 0;
             float slope = 0.0f;
             if (r < nrows) {
@@ -571,11 +557,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                 visible_keys(p, pos, pc->len, lo, hi);
                 if (MOD && p.slopes) slope = __ldg(p.slopes + head) * kLog2e;
             }
-            // this half's first tile (of every second one)
-            const int j1 = a + (both && ((a - pc->k0) & 1) != h ? 1 : 0);
             float m = -INFINITY, l = 0.0f;
 #pragma unroll 1
-            for (int j = j1; j < e && wait.ok; j += 1 + both, ++ns) {
+            for (int j = a; j < e && wait.ok; ++j, ++ns) {
                 const int u2 = ns & 1;                   // which P of the half
                 const uint32_t tp = tp0 + u2 * 32;
                 if (!warp_wait_all(wait, s_addr(&bars.s_full[h]), (uint32_t)ns & 1u)) break;
@@ -614,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                 if (__any_sync(0xFFFFFFFFu, raise)) {
                     const float f = raise ? (m == -INFINITY ? 0.0f : ex2(m - mx)) : 1.0f;
                     if (raise) { m = mx; l *= f; }
-                    if (j > j1) {
+                    if (j > a) {
                         if (!warp_wait_all(wait, s_addr(&bars.pv_done[h][u2 ^ 1]), (uint32_t)((ns - 1) >> 1) & 1u)) break;
                         tc_after();
 #pragma unroll 1
@@ -658,40 +642,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
             }
             if (!wait.ok) break;
             // ---- the rows' result ----------------------------------------------
-            bool any = e > j1;
+            const bool any = e > a;
             if (any && !warp_wait_all(wait, s_addr(&bars.pv_done[h][(ns - 1) & 1]), (uint32_t)((ns - 1) >> 1) & 1u)) break;
             tc_after();
-            // Shared rows: half 1 leaves its part where it is (the warps of both
-            // halves reach the same lanes of tensor memory) and half 0 adds it up.
-            bool other = false;
-            float f0 = 1.0f, f1 = 0.0f;
-            if (both) {
-                const uint32_t tml = tm + 128 + 64 + lane_base;      // half 1's first weights, done with
-                const uint32_t full = s_addr(&bars.both_full[warp & 3]), empty = s_addr(&bars.both_empty[warp & 3]);
-                const uint32_t ph = (uint32_t)nb++ & 1u;
-                if (h == 1) {
-                    tm_st2(tml, m, l);
-                    tm_wait_st();
-                    tc_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive1(&bars.both_full[warp & 3]);
-                    if (!warp_wait_all(wait, empty, ph)) break;
-                    tc_after();
-                    done();
-                    continue;
-                }
-                if (!warp_wait_all(wait, full, ph)) break;
-                tc_after();
-                float2 x;
-                tm_ld2(tml, x.x, x.y);
-                tm_wait_ld();
-                const float M = fmaxf(m, x.x);
-                f0 = part_weight(m, l, M);
-                f1 = part_weight(x.x, x.y, M);
-                l = fmaf(l, f0, x.y * f1);
-                m = M;
-                other = a + (((a - pc->k0) & 1) != 1 ? 1 : 0) < e;
-            }
             const bool mine = r < nrows, empty = l == 0.0f, part = pc->shared;
             const float inv = empty ? 0.0f : 1.0f / l;
             const long long row = pc->t0 + ti;
@@ -706,18 +659,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                 float o[16];
                 __syncwarp();
                 if (any) { tm_ld16(to + c, o); tm_wait_ld(); }
-                if (both) {
-#pragma unroll
-                    for (int u = 0; u < 16; ++u) o[u] = any ? o[u] * f0 : 0.0f;
-                    if (other) {
-                        float o1[16];
-                        __syncwarp();
-                        tm_ld16(to + DP + c, o1);
-                        tm_wait_ld();
-#pragma unroll
-                        for (int u = 0; u < 16; ++u) o[u] = fmaf(o1[u], f1, o[u]);
-                    }
-                }
 #pragma unroll
                 for (int u = 0; u < 16; ++u) odd |= !(fabsf(o[u]) < INFINITY);
                 if (empty) {
@@ -734,11 +675,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                 }
             }
             tc_before();
-            if (both) {                                  // half 1's sums have been read
-                any = any || other;
-                __syncwarp();
-                if (lane == 0) mbar_arrive1(&bars.both_empty[warp & 3]);
-            }
             if (mine && part) {
                 __stcg(so + (size_t)kRows * p.D + at, m);
                 __stcg(so + (size_t)kRows * p.D + kRows + at, l);
