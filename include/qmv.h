@@ -607,9 +607,9 @@ int qmv_describe_plan(int family, int M, int N, int K, int bits, int group_size,
  * (1: a consumer warp gave up on a ring stage, 2: the producer warp gave up on
  * a free stage, 4: the producer gave up waiting for its own copies, 8 and 16:
  * the warps that issue products or hand out work) and the call that hit it
- * leaves y (out, lse) undefined, and an attention workspace to be cleared.  Writes the word to *code and, if clear != 0,
- * resets it to zero.  Synchronous: it waits for the device's pending work
- * (cudaMemcpyFromSymbol).  Returns QMV_OK, QMV_EINVAL (code NULL) or QMV_ECUDA.
+ * leaves y (out, lse) undefined, and an attention workspace to be cleared.
+ * Writes the word to *code and, if clear != 0, resets it to zero.  Synchronous:
+ * it waits for the device's pending work (cudaMemcpyFromSymbol).  Returns QMV_OK, QMV_EINVAL (code NULL) or QMV_ECUDA.
  */
 int qmv_device_fault(unsigned int* code, int clear);
 

@@ -106,12 +106,11 @@ cudaError_t launch_attn_rows(int dtype, const AttnParams& p, cudaStream_t st) {
     const long long rows = (long long)p.T * p.Hq;
     long long grid = (rows + kRowWarps - 1) / kRowWarps;
     if (grid > (1 << 20)) grid = 1 << 20;
-    static std::atomic<unsigned> none{0};
     const dim3 g((unsigned)grid), blk(kRowWarps * 32);
     switch (dtype) {
-        case 0: return launch_dependent(attn_rows_kernel<float>, none, 0, g, blk, 0, st, p);
-        case 1: return launch_dependent(attn_rows_kernel<__half>, none, 0, g, blk, 0, st, p);
-        case 2: return launch_dependent(attn_rows_kernel<__nv_bfloat16>, none, 0, g, blk, 0, st, p);
+        case 0: return launch_dependent(attn_rows_kernel<float>, g, blk, 0, st, p);
+        case 1: return launch_dependent(attn_rows_kernel<__half>, g, blk, 0, st, p);
+        case 2: return launch_dependent(attn_rows_kernel<__nv_bfloat16>, g, blk, 0, st, p);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -14,8 +14,9 @@
 // tiles' time each.  Few tiles a block are therefore cut at the units' own ends
 // (every unit into parts of Q tiles, the last one shorter), if that gives no more
 // parts than blocks at the even share or 5/4 of it; failing that, in eighths of
-// the even share (at least 4 tiles), so that short units stay whole.  (Parts of up
-// to twice the share: 12 fp32 sequences of 100-2100 keys 56 us, so 48.)
+// the even share (at least 4 tiles), so that short units stay whole.  (12 fp32
+// sequences of 100-2100 keys: 46 us, and 54 with whole parts of up to twice the share
+// and quarters.)
 //
 // A block whose part ends or begins inside a unit leaves that unit's partial
 // result (unnormalised sums, maxima, weights) in the workspace and counts

@@ -106,20 +106,23 @@ __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepco
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // -------------------------------------------------------------- host side --
-// Launch with programmatic dependent launch: the kernel may begin while the
-// kernel before it drains, and waits for it before it touches memory.
-template <class Kern, class P>
-inline cudaError_t launch_dependent(Kern kern, std::atomic<unsigned>& configured, int smem_max, dim3 grid, dim3 block,
-                                    size_t smem, cudaStream_t st, const P& p) {
+// Lets a kernel use `smem` bytes of dynamic shared memory, once per device.
+template <class Kern>
+inline cudaError_t allow_smem(Kern kern, std::atomic<unsigned>& configured, int smem) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const unsigned bit = 1u << (dev & 31);
-    if (smem_max > 48 * 1024 && !(configured.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max);
-        if (e != cudaSuccess) return e;
-        configured.fetch_or(bit, std::memory_order_acq_rel);
-    }
+    if (configured.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) configured.fetch_or(bit, std::memory_order_acq_rel);
+    return e;
+}
+
+// Launch with programmatic dependent launch: the kernel may begin while the
+// kernel before it drains, and waits for it before it touches memory.
+template <class Kern, class... Args>
+inline cudaError_t launch_dependent(Kern kern, dim3 grid, dim3 block, size_t smem, cudaStream_t st, const Args&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
@@ -130,7 +133,15 @@ inline cudaError_t launch_dependent(Kern kern, std::atomic<unsigned>& configured
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p);
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// log2 of the page size, -1 if it is no power of two.
+inline int page_shift_of(int page) {
+    if (page & (page - 1)) return -1;
+    int s = 0;
+    while ((1 << s) < page) ++s;
+    return s;
 }
 
 cudaError_t launch_rope(int dtype, const RopeParams& p, int vec_bytes, cudaStream_t st);

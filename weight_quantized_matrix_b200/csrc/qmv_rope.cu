@@ -249,17 +249,8 @@ template <class T, int E> cudaError_t launch_te(const RopeParams& p, cudaStream_
     g.by_tok = make_div(per_tok, tpb * per_tok);
     g.by_rot = make_div(ipr_rot, per_tok);
     g.by_copy = make_div(ipr_copy, per_tok);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;       // at most 32 tokens x 128 pairs x 8 bytes = 32 KB
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, rope_kernel<T, E>, p, g);
+    // smem: at most 32 tokens x 128 pairs x 8 bytes = 32 KB
+    return launch_dependent(rope_kernel<T, E>, dim3((unsigned)grid), dim3(kThreads), smem, st, p, g);
 }
 
 template <class T> cudaError_t launch_t(const RopeParams& p, int vec_bytes, cudaStream_t st) {
