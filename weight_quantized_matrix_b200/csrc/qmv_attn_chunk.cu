@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     constexpr uint32_t tm = 0;                   // all 512 columns: tensor memory's start
 
     Sched<kRows, kTile> sc;
-    sc.template init<kThreads, 32>(p, sm, 8);
+    sc.template init<kThreads>(p, sm, 8);
 
     // Pieces are read in order by every role but the scheduling warp: take()
     // waits for the next one, done() gives it back.

@@ -28,10 +28,10 @@ namespace {
 constexpr int kRows = 16;
 
 template <int DP> struct F32Geom {
-    static constexpr int WARPS = DP == 256 ? 2 : 4;
+    static constexpr int WARPS = DP == 64 ? 4 : 2;
     static constexpr int TILE = 16 * WARPS;
     static constexpr int STAGES = 3;
-    static constexpr int PER_SM = DP == 64 ? 2 : 1;
+    static constexpr int PER_SM = DP == 256 ? 1 : 2;
     static constexpr int ROWB = DP * 4;
     static constexpr int STEP = 2 * 16 * ROWB;
     static constexpr int RING = WARPS * STAGES * STEP;
@@ -71,10 +71,19 @@ __device__ __forceinline__ void f32_step(const unsigned char* kb, const unsigned
         }
     }
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        x[r] += __shfl_xor_sync(0xFFFFFFFFu, x[r], 16);
-        if constexpr (MOD) x[r] = mod.apply(x[r], rows.slope[r], j - rows.pos[r]);
-        else x[r] *= mod.pre;
+    for (int r = 0; r < R; ++r) x[r] += __shfl_xor_sync(0xFFFFFFFFu, x[r], 16);
+    if constexpr (MOD) {                        // each half of the warp takes half of the rows
+#pragma unroll
+        for (int r = 0; r < R / 2; ++r) {
+            const int mr = hf ? r + R / 2 : r;
+            const float y = mod.apply(hf ? x[r + R / 2] : x[r], rows.slope[mr], j - rows.pos[mr]);
+            const float z = __shfl_xor_sync(0xFFFFFFFFu, y, 16);
+            x[r] = hf ? z : y;
+            x[r + R / 2] = hf ? y : z;
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < R; ++r) x[r] *= mod.pre;
     }
     if (!full) {
 #pragma unroll
@@ -129,7 +138,17 @@ __device__ __forceinline__ void f32_step(const unsigned char* kb, const unsigned
                 }
             }
         }
-        if (full) {
+        // Unseen keys weigh exactly 0, which finite values leave 0.
+        bool plain = full;
+        if (!full) {
+            float z = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int u = 0; u < VEC; ++u) z = fmaf(v[k][u], 0.0f, z);
+            plain = __all_sync(0xFFFFFFFFu, z == 0.0f);
+        }
+        if (plain) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const float4 w = *reinterpret_cast<const float4*>(&s_p[r][k4]);
@@ -178,7 +197,7 @@ attn_f32_kernel(const __grid_constant__ AttnParams p, int page_shift) {
     grid_launch_dependents();
 
     Sched<kRows, Gm::TILE> sc;
-    sc.template init<NTH, 1>(p, sm, 12);
+    sc.template init<NTH>(p, sm, 12);
     const ScoreMod<true> mod(p);
     const int page16 = (int)(p.page_s / 4), tok16 = (int)(p.tok_s / 4);
 

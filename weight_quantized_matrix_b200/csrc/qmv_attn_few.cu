@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(WARPS * 32, FewGeom<DP, WARPS>::PER_SM) attn_f
     grid_launch_dependents();
 
     Sched<kRows, Gm::TILE> sc;
-    sc.template init<WARPS * 32, 1>(p, sm, 768 / Gm::TILE);
+    sc.template init<WARPS * 32>(p, sm, 768 / Gm::TILE);
     const ScoreMod<false> mod(p);
     const float scale2 = p.scale * kLog2e;
     const int page16 = (int)(p.page_s / 8), tok16 = (int)(p.tok_s / 8);

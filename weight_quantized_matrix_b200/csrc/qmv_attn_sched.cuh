@@ -114,28 +114,38 @@ template <int ROWS, int TK> struct Sched {
         }
         load_unit(p);
     }
-    // Every thread of the block calls this (NT threads, LPS lanes a sequence).
-    template <int NT, int LPS> __device__ __forceinline__ void init(const AttnParams& p, SchedSmem& sm, int min_tiles) {
-        constexpr int SEQS = NT / LPS;
-        const int tid = threadIdx.x, lane = tid & 31, sub = tid % LPS;
-        int only = -1;          // tiles of the thread's sequence where it has one row tile and there is one round
-        const int rounds = (p.n_seqs + SEQS - 1) / SEQS;
+    // Every thread of the block calls this (NT threads).  A sequence's units are
+    // counted by 1 to 32 lanes, as many as leave every sequence a place in one
+    // round (one lane for all 60 units of 120 tokens x 8 heads: the call takes 44 us,
+    // so 24).
+    template <int NT> __device__ __forceinline__ void init(const AttnParams& p, SchedSmem& sm, int min_tiles) {
+        const int tid = threadIdx.x, lane = tid & 31;
+        int lg = 5;
+        while (lg > 0 && (long long)p.n_seqs << lg > NT) --lg;
+        const int lps = 1 << lg, sub = tid & (lps - 1), seqs = NT >> lg;
+        const int rounds = (p.n_seqs + seqs - 1) >> (__ffs(seqs) - 1);
+        int kept = -2;          // tiles of the lane's only unit, -1 for none, in the one round; -2: not known
         auto cost = [&](int bb) {
             int v = 0;
-            if (LPS == 1 && only >= 0) return chunks(only);
-            if (bb < p.n_seqs) {
+            if (kept >= -1) {
+                if (kept >= 0) v = chunks(kept);
+            } else if (bb < p.n_seqs) {
                 const SeqInfo si = seq_info(p, bb);
                 const int nq = (si.n * p.G + ROWS - 1) / ROWS;
+                if (nq <= lps && rounds == 1) kept = -1;
                 int f;
 #pragma unroll 1
-                for (int k = sub; k < nq; k += LPS) {
+                for (int k = sub; k < nq; k += lps) {
                     const int tiles = unit_tiles<ROWS, TK>(p, si, k, f);
-                    if (nq == 1 && rounds == 1) only = tiles;
+                    if (kept == -1) kept = tiles;
                     v += chunks(tiles);
                 }
             }
-#pragma unroll
-            for (int w = LPS / 2; w > 0; w >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, w);
+            // one unit a sequence: its first lane, which alone is read, holds the sum
+            if (__any_sync(0xFFFFFFFFu, sub != 0 && v != 0)) {
+#pragma unroll 1
+                for (int w = lps >> 1; w > 0; w >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, w);
+            }
             return v;
         };
         // inclusive scan over the block (the value counts once a sequence)
@@ -170,7 +180,7 @@ template <int ROWS, int TK> struct Sched {
             all = 0;
 #pragma unroll 1
             for (int r = 0; r < rounds; ++r) {
-                v = cost(r * SEQS + tid / LPS);
+                v = cost(r * seqs + (tid >> lg));
                 long long total;
                 incl = scan(v, total);
                 all += total;
@@ -207,12 +217,12 @@ template <int ROWS, int TK> struct Sched {
         for (int r = 0; r < rounds; ++r) {
             long long total = all;
             if (rounds > 1) {
-                v = cost(r * SEQS + tid / LPS);
+                v = cost(r * seqs + (tid >> lg));
                 incl = scan(v, total);
             }
             const long long end = base + incl, beg = end - (long long)v * p.Hkv;
             if (sub == 0 && beg <= w0 && w0 < end) {
-                sm.seq = r * SEQS + tid / LPS;
+                sm.seq = r * seqs + (tid >> lg);
                 sm.seq_at = beg;
                 sm.per_head = v;
             }
@@ -225,14 +235,28 @@ template <int ROWS, int TK> struct Sched {
         int off = w0 - (int)sm.seq_at;
         h = off / sm.per_head;
         off -= h * sm.per_head;
-        i = -1;
-        c = 0;
+        i = 0;
+        if (s.n * p.G > ROWS) {             // 32 units at a time
 #pragma unroll 1
-        do {
-            off -= c;
-            ++i;
-            load_unit(p);
-        } while (off >= c);
+            for (;; i += 32) {
+                int f, cc = 0;
+                if ((i + lane) * ROWS < s.n * p.G) cc = chunks(unit_tiles<ROWS, TK>(p, s, i + lane, f));
+                int upto = cc;
+#pragma unroll
+                for (int w = 1; w < 32; w <<= 1) {
+                    const int u = __shfl_up_sync(0xFFFFFFFFu, upto, w);
+                    if (lane >= w) upto += u;
+                }
+                const unsigned here = __ballot_sync(0xFFFFFFFFu, off < upto);
+                const int at = here ? __ffs(here) - 1 : 31;
+                off -= __shfl_sync(0xFFFFFFFFu, here ? upto - cc : upto, at);
+                if (here || (i + 32) * ROWS >= s.n * p.G) {     // (the bound: lists that change meanwhile end, too)
+                    i += at;
+                    break;
+                }
+            }
+        }
+        load_unit(p);
         us = w0 - off;
         live = true;
         if (!split && off > 0) next(p);     // the unit belongs to the block before
