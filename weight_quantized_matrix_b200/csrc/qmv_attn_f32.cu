@@ -7,15 +7,17 @@
 // reads that feed them.
 //  * As in qmv_attn_few.cu every warp streams its own 16 keys of a tile through its
 //    own ring (cp.async, 16-byte chunks, XOR-swizzled).
-//  * Scores: lane = (key, half of the dims); a 16-byte read of the key serves up to
-//    16 rows, whose queries are broadcast reads.  Units of up to 4, 8 or 16 rows
-//    run code of that size.
+//  * Scores: a lane makes 4 keys of up to 4 rows from half of the dims, so that
+//    shared memory feeds the FMAs.  Units of up to 4, 8 or 16 rows run code of
+//    that size.
 //  * Weights go through shared memory; for the second product a lane owns D / 32
 //    dims of every row, V is read once for all rows.
 //  * DP = 64, 128 or 256 dims, padded with zeros in shared memory only.
-// Measured: 12 sequences of 2-5 new tokens over 100-2100 keys, 16 heads of 64: 46 us =
-// 2.6 TB/s, bound by the latency of a step's instructions; 76 with one code for
-// all row counts, 57 before whole tiles were copied without masks and shares cut finer.
+// Measured: 12 sequences of 2-5 new tokens over 100-2100 keys, 16 heads of 64: 43 us =
+// 2.8 TB/s; one token of 8 sequences over 4000 keys, 8 kv heads of 128, 74 us = 3.5 TB/s:
+// bound by the latency of a step's instructions, at one or two warps a scheduler.
+// 1000 tokens over 2000 keys, 32 heads of 128: 1127 us = 22 TFLOP/s, so bound, too
+// (FMA pipe 35 % busy); 1290 with a lane a key and all rows.
 #include <algorithm>
 
 #include "qmv_attn_mma.cuh"
@@ -46,14 +48,16 @@ struct Rows {
     float slope[kRows];
 };
 
-// One step: 16 keys (j0 on) against the first R rows.  Scores with lane = (key,
-// half of the dims), weights through s_p, second product with lane = dims.
-template <int DP, bool MOD, int R>
-__device__ __forceinline__ void f32_step(const unsigned char* kb, const unsigned char* vb, const float* s_q, float (&s_p)[kRows][16],
-                                         const Rows& rows, const ScoreMod<true>& mod, int j0, bool full, float (&o)[kRows][DP / 32],
-                                         float (&m)[kRows], float (&l)[kRows]) {
+// The weights of the first 4 rows: lane = (key, half of the dims) makes its key's
+// scores of all rows (few rows want the reads in flight, not their reuse: one
+// token of 32 heads on 8 over 8 x 4000 keys takes 75 us this way and 82 the other).
+// m and l are all rows', l of the lane's key.
+template <int DP, bool MOD>
+__device__ __forceinline__ void f32_weights4(const unsigned char* kb, const float* s_q, float (&s_p)[16][kRows], const Rows& rows,
+                                             const ScoreMod<true>& mod, int j0, bool full, float2 (&o)[kRows / 2][DP / 32],
+                                             float (&m)[kRows / 4], float (&l)[kRows / 4]) {
     using Gm = F32Geom<DP>;
-    constexpr int ROWB = Gm::ROWB, CPR = DP / 4, VEC = DP / 32;
+    constexpr int R = 4, ROWB = Gm::ROWB, CPR = DP / 4, VEC = DP / 32;
     const int lane = threadIdx.x & 31, key = lane & 15, hf = lane >> 4, j = j0 + key;
     float x[R], mx[R];
 #pragma unroll
@@ -90,7 +94,6 @@ __device__ __forceinline__ void f32_step(const unsigned char* kb, const unsigned
         for (int r = 0; r < R; ++r)
             if (j < rows.lo[r] || j >= rows.hi[r]) x[r] = -INFINITY;
     }
-    // all rows' maxima side by side: a butterfly's latency is paid once
 #pragma unroll
     for (int r = 0; r < R; ++r) mx[r] = x[r];
 #pragma unroll
@@ -104,36 +107,164 @@ __device__ __forceinline__ void f32_step(const unsigned char* kb, const unsigned
         raise |= mx[r] > m[r];
     }
     if (raise) {                                // the same for every lane
+        float f[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const float f = mx[r] > m[r] ? ex2(m[r] - mx[r]) : 1.0f;
-            l[r] *= f;
-#pragma unroll
-            for (int u = 0; u < VEC; ++u) o[r][u] *= f;
+            f[r] = mx[r] > m[r] ? ex2(m[r] - mx[r]) : 1.0f;
+            l[r] *= f[r];
             m[r] = mx[r];
+        }
+#pragma unroll
+        for (int u = 0; u < VEC; ++u) {
+            o[0][u] = mul2(o[0][u], make_float2(f[0], f[1]));
+            o[1][u] = mul2(o[1][u], make_float2(f[2], f[3]));
         }
     }
     __syncwarp();
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const float e = ex2(x[r] - (mx[r] == -INFINITY ? 0.0f : mx[r]));
-        l[r] += e;                              // summed over the 16 lanes of a half at the end
-        if (hf == 0) s_p[r][key] = e;
+        x[r] = ex2(x[r] - (mx[r] == -INFINITY ? 0.0f : mx[r]));
+        l[r] += x[r];                           // summed over the 16 lanes of a half at the end
+    }
+    if (hf == 0) *reinterpret_cast<float4*>(&s_p[4 * (key & 3) + (key >> 2)][0]) = make_float4(x[0], x[1], x[2], x[3]);
+    __syncwarp();
+}
+
+// The weights of a step of 16 keys (j0 on) against the first R = 8 or 16 rows: lane = (kl, rg,
+// hf) makes keys kl + 4 i, i < 4, of rows rg + 4 r from half hf of the dims: 8
+// 16-byte reads without conflicts feed 64 products (R = 16; with a lane a key and
+// all rows it is 17).  The halves then swap sums, and each goes on with two of the
+// keys; m and l are the lane's rows'.  Weights go through s_p, key kl + 4 i at
+// 4 kl + i, row rg + 4 r at rg RL + r.
+template <int DP, bool MOD, int R>
+__device__ __forceinline__ void f32_weights(const unsigned char* kb, const float* s_q, float (&s_p)[16][kRows],
+                                         float (&s_f)[kRows], const Rows& rows, const ScoreMod<true>& mod, int j0, bool full,
+                                         float2 (&o)[kRows / 2][DP / 32], float (&m)[kRows / 4], float (&l)[kRows / 4]) {
+    using Gm = F32Geom<DP>;
+    constexpr int ROWB = Gm::ROWB, CPR = DP / 4, VEC = DP / 32, RL = R / 4;
+    const int lane = threadIdx.x & 31, kl = lane & 3, rg = (lane >> 2) & 3, hf = lane >> 4;
+    float2 s[4][RL];            // even and odd dims
+    float x[2][RL], mx[RL];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < RL; ++r) s[i][r] = make_float2(0.0f, 0.0f);
+#pragma unroll 2
+    for (int c = 0; c < CPR / 2; ++c) {
+        const int cc = hf * (CPR / 2) + (c ^ (hf << 2));        // the halves read other banks
+        float4 kv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int key = kl + 4 * i;
+            kv[i] = *reinterpret_cast<const float4*>(kb + key * ROWB + ((cc ^ (key & 7)) << 4));
+        }
+#pragma unroll
+        for (int r = 0; r < RL; ++r) {
+            const float4 qv = *reinterpret_cast<const float4*>(s_q + ((rg + 4 * r) * 2 + hf) * Gm::QH + (c ^ (hf << 2)) * 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[i][r] = fma2(make_float2(qv.x, qv.y), make_float2(kv[i].x, kv[i].y), s[i][r]);
+                s[i][r] = fma2(make_float2(qv.z, qv.w), make_float2(kv[i].z, kv[i].w), s[i][r]);
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < RL; ++r)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const float a = s[u][r].x + s[u][r].y, b = s[2 + u][r].x + s[2 + u][r].y;
+            x[u][r] = (hf ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, hf ? a : b, 16);
+        }
+    const int j = j0 + kl + 8 * hf;                             // the lane's keys: j and j + 4
+#pragma unroll
+    for (int r = 0; r < RL; ++r)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if constexpr (MOD) x[u][r] = mod.apply(x[u][r], rows.slope[rg + 4 * r], j + 4 * u - rows.pos[rg + 4 * r]);
+            else x[u][r] *= mod.pre;
+        }
+    if (!full) {
+#pragma unroll
+        for (int r = 0; r < RL; ++r) {
+            const int lo = rows.lo[rg + 4 * r], hi = rows.hi[rg + 4 * r];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                if (j + 4 * u < lo || j + 4 * u >= hi) x[u][r] = -INFINITY;
+        }
+    }
+    // all rows' maxima side by side: a butterfly's latency is paid once
+    bool raise = false;
+#pragma unroll
+    for (int r = 0; r < RL; ++r) mx[r] = fmaxf(x[0][r], x[1][r]);
+#pragma unroll
+    for (int w = 1; w <= 16; w = w == 2 ? 16 : w * 2)
+#pragma unroll
+        for (int r = 0; r < RL; ++r) mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xFFFFFFFFu, mx[r], w));
+#pragma unroll
+    for (int r = 0; r < RL; ++r) {
+        mx[r] = fmaxf(mx[r], m[r]);
+        raise |= mx[r] > m[r];
+    }
+    raise = __any_sync(0xFFFFFFFFu, raise);
+    __syncwarp();                               // every lane is done with s_p and s_f
+    if (raise) {
+#pragma unroll
+        for (int r = 0; r < RL; ++r) {
+            const float f = mx[r] > m[r] ? ex2(m[r] - mx[r]) : 1.0f;
+            l[r] *= f;
+            m[r] = mx[r];
+            if (kl == 0 && hf == 0) s_f[rg * RL + r] = f;
+        }
     }
     __syncwarp();
+#pragma unroll
+    for (int r = 0; r < RL; ++r) {
+        const float ref = mx[r] == -INFINITY ? 0.0f : mx[r];
+        const float e0 = ex2(x[0][r] - ref), e1 = ex2(x[1][r] - ref);
+        l[r] += e0 + e1;                        // summed over the row's 8 lanes at the end
+        x[0][r] = e0;
+        x[1][r] = e1;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        float* to = &s_p[4 * kl + 2 * hf + u][rg * RL];
+        if constexpr (RL == 4) *reinterpret_cast<float4*>(to) = make_float4(x[u][0], x[u][1], x[u][2], x[u][3]);
+        else *reinterpret_cast<float2*>(to) = make_float2(x[u][0], x[u][1]);
+    }
+    __syncwarp();
+    if (raise) {
+#pragma unroll
+        for (int r = 0; r < R / 2; ++r) {
+            const float2 f = *reinterpret_cast<const float2*>(&s_f[2 * r]);
+#pragma unroll
+            for (int u = 0; u < VEC; ++u) o[r][u] = mul2(o[r][u], f);
+        }
+    }
+}
+
+// One step: weights, then the second product with lane = dims, two rows to an FMA.
+template <int DP, bool MOD, int R>
+__device__ __forceinline__ void f32_step(const unsigned char* kb, const unsigned char* vb, const float* s_q, float (&s_p)[16][kRows],
+                                         float (&s_f)[kRows], const Rows& rows, const ScoreMod<true>& mod, int j0, bool full,
+                                         float2 (&o)[kRows / 2][DP / 32], float (&m)[kRows / 4], float (&l)[kRows / 4]) {
+    constexpr int ROWB = F32Geom<DP>::ROWB, VEC = DP / 32, RL = R / 4;
+    const int lane = threadIdx.x & 31;
+    if constexpr (R == 4) f32_weights4<DP, MOD>(kb, s_q, s_p, rows, mod, j0, full, o, m, l);
+    else f32_weights<DP, MOD, R>(kb, s_q, s_p, s_f, rows, mod, j0, full, o, m, l);
 #pragma unroll 2
     for (int k4 = 0; k4 < 16; k4 += 4) {
         float v[4][VEC];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const unsigned char* row = vb + (k4 + k) * ROWB;
+            const int key = k4 / 4 + 4 * k;
+            const unsigned char* row = vb + key * ROWB;
             if constexpr (VEC == 2) {
-                const float2 f = *reinterpret_cast<const float2*>(row + (((lane >> 1) ^ ((k4 + k) & 7)) << 4) + (lane & 1) * 8);
+                const float2 f = *reinterpret_cast<const float2*>(row + (((lane >> 1) ^ (key & 7)) << 4) + (lane & 1) * 8);
                 v[k][0] = f.x; v[k][1] = f.y;
             } else {
 #pragma unroll
                 for (int u = 0; u < VEC; u += 4) {
-                    const float4 f = *reinterpret_cast<const float4*>(row + (((lane + u * 8) ^ ((k4 + k) & 7)) << 4));
+                    const float4 f = *reinterpret_cast<const float4*>(row + (((lane + u * 8) ^ (key & 7)) << 4));
                     v[k][u] = f.x; v[k][u + 1] = f.y; v[k][u + 2] = f.z; v[k][u + 3] = f.w;
                 }
             }
@@ -150,27 +281,35 @@ __device__ __forceinline__ void f32_step(const unsigned char* kb, const unsigned
         }
         if (plain) {
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float4 w = *reinterpret_cast<const float4*>(&s_p[r][k4]);
+            for (int k = 0; k < 4; ++k) {
+                float2 vv[VEC];
 #pragma unroll
-                for (int u = 0; u < VEC; ++u) {
-                    o[r][u] = fmaf(w.x, v[0][u], o[r][u]);
-                    o[r][u] = fmaf(w.y, v[1][u], o[r][u]);
-                    o[r][u] = fmaf(w.z, v[2][u], o[r][u]);
-                    o[r][u] = fmaf(w.w, v[3][u], o[r][u]);
+                for (int u = 0; u < VEC; ++u) vv[u] = make_float2(v[k][u], v[k][u]);
+#pragma unroll
+                for (int r = 0; r < R; r += 4) {
+                    const float4 w = *reinterpret_cast<const float4*>(&s_p[k4 + k][r]);
+#pragma unroll
+                    for (int u = 0; u < VEC; ++u) {
+                        o[r / 2][u] = fma2(make_float2(w.x, w.y), vv[u], o[r / 2][u]);
+                        o[r / 2 + 1][u] = fma2(make_float2(w.z, w.w), vv[u], o[r / 2 + 1][u]);
+                    }
                 }
             }
         } else {
             // a key the row does not see takes no part, whatever its value holds
 #pragma unroll
             for (int r = 0; r < R; ++r) {
+                const int lo = rows.lo[r / RL + 4 * (r % RL)], hi = rows.hi[r / RL + 4 * (r % RL)];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int jk = j0 + k4 + k;
-                    if (jk < rows.lo[r] || jk >= rows.hi[r]) continue;
-                    const float w = s_p[r][k4 + k];
+                    const int jk = j0 + k4 / 4 + 4 * k;
+                    if (jk < lo || jk >= hi) continue;
+                    const float w = s_p[k4 + k][r];
 #pragma unroll
-                    for (int u = 0; u < VEC; ++u) o[r][u] = fmaf(w, v[k][u], o[r][u]);
+                    for (int u = 0; u < VEC; ++u) {
+                        float& d = r % 2 ? o[r / 2][u].y : o[r / 2][u].x;
+                        d = fmaf(w, v[k][u], d);
+                    }
                 }
             }
         }
@@ -185,7 +324,8 @@ attn_f32_kernel(const __grid_constant__ AttnParams p, int page_shift) {
     extern __shared__ __align__(1024) unsigned char ring[];
     float* s_q = reinterpret_cast<float*>(ring + Gm::RING);
     __shared__ SchedSmem sm;
-    __shared__ __align__(16) float s_p[WARPS][kRows][16];
+    __shared__ __align__(16) float s_p[WARPS][16][kRows];
+    __shared__ __align__(16) float s_f[WARPS][kRows];
     __shared__ float s_m[WARPS][kRows], s_l[WARPS][kRows];
     __shared__ Rows rows;
     __shared__ int s_flag;
@@ -291,13 +431,17 @@ attn_f32_kernel(const __grid_constant__ AttnParams p, int page_shift) {
         // keys that every row sees (bounds ascend with the row)
         const int alo = rows.lo[nrows - 1], ahi = rows.hi[0];
 
-        float o[kRows][VEC], m[kRows], l[kRows];
+        float2 o[kRows / 2][VEC];
+        float m[kRows / 4], l[kRows / 4];        // of rows r (4 rows), (lane / 4) % 4 + 4 r (more)
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
+        for (int r = 0; r < kRows / 4; ++r) {
             m[r] = -INFINITY;
             l[r] = 0.0f;
+        }
 #pragma unroll
-            for (int u = 0; u < VEC; ++u) o[r][u] = 0.0f;
+        for (int r = 0; r < kRows / 2; ++r) {
+#pragma unroll
+            for (int u = 0; u < VEC; ++u) o[r][u] = make_float2(0.0f, 0.0f);
         }
         // the first STAGES - 1 rounds only fill the ring
         int slot = 0, fill = 0;
@@ -318,27 +462,43 @@ attn_f32_kernel(const __grid_constant__ AttnParams p, int page_shift) {
             const bool full = j0 >= alo && j0 + 16 <= ahi;
 
             // as many rows as the unit has, in fours
-            if (nrows <= 4) f32_step<DP, MOD, 4>(kb, vb, s_q, s_p[warp], rows, mod, j0, full, o, m, l);
-            else if (nrows <= 8) f32_step<DP, MOD, 8>(kb, vb, s_q, s_p[warp], rows, mod, j0, full, o, m, l);
-            else f32_step<DP, MOD, 16>(kb, vb, s_q, s_p[warp], rows, mod, j0, full, o, m, l);
+            if (nrows <= 4) f32_step<DP, MOD, 4>(kb, vb, s_q, s_p[warp], s_f[warp], rows, mod, j0, full, o, m, l);
+            else if (nrows <= 8) f32_step<DP, MOD, 8>(kb, vb, s_q, s_p[warp], s_f[warp], rows, mod, j0, full, o, m, l);
+            else f32_step<DP, MOD, 16>(kb, vb, s_q, s_p[warp], s_f[warp], rows, mod, j0, full, o, m, l);
         }
         cp_wait<0>();
         __syncthreads();
 
         // ---- the warps' results meet in the ring ------------------------------
         float* red = reinterpret_cast<float*>(ring);            // [warp][row][DP]
+        const int lg_rl = nrows <= 4 ? 0 : nrows <= 8 ? 1 : 2;
+#pragma unroll
+        for (int r = 0; r < kRows / 4; ++r) {
+            l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 2);
+            if (nrows <= 4) {
+                l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 4);
+                l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 8);
+                if (lane == 0) { s_m[warp][r] = m[r]; s_l[warp][r] = l[r]; }
+            } else {
+                l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 16);
+                const int at_row = (lane >> 2 & 3) + 4 * r;
+                if ((lane & 0x13) == 0) { s_m[warp][at_row] = m[r]; s_l[warp][at_row] = l[r]; }
+            }
+        }
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
+            if (r >= 4 << lg_rl) break;         // places no step filled
+            float* d = red + (warp * kRows + (r >> lg_rl) + 4 * (r & ((1 << lg_rl) - 1))) * DP;
+            float e[VEC];
 #pragma unroll
-            for (int w = 8; w > 0; w >>= 1) l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], w);
-            if (lane == 0) { s_m[warp][r] = m[r]; s_l[warp][r] = l[r]; }
-            float* d = red + (warp * kRows + r) * DP;
+            for (int u = 0; u < VEC; ++u) e[u] = r % 2 ? o[r / 2][u].y : o[r / 2][u].x;
             if constexpr (VEC == 2) {
-                *reinterpret_cast<float2*>(d + lane * 2) = make_float2(o[r][0], o[r][1]);
+                *reinterpret_cast<float2*>(d + lane * 2) = make_float2(e[0], e[1]);
             } else {
 #pragma unroll
                 for (int u = 0; u < VEC; u += 4)
-                    *reinterpret_cast<float4*>(d + (lane + u * 8) * 4) = make_float4(o[r][u], o[r][u + 1], o[r][u + 2], o[r][u + 3]);
+                    *reinterpret_cast<float4*>(d + (lane + u * 8) * 4) = make_float4(e[u], e[u + 1], e[u + 2], e[u + 3]);
             }
         }
         __syncthreads();

@@ -62,15 +62,20 @@ int check_cache(const qmv_paged_kv* kv) {
 // Which kernel of the 16-bit types: 16 rows a kv head and unit, keys streamed by
 // warp, or 256 rows on the tensor cores.  Measured, heads of 128, 4 query heads
 // a kv head (us, few / many): 32 sequences of 4000 keys, 16 rows 90 / 137, 24
-// rows 175 / 138; one of 100000, 32 rows 141 / 164, 48 rows 200 / 167; one
-// of 2000, 96 rows 23 / 32.  So: up to 16 rows the first; up to 32 while its
-// units leave SMs free (it reads keys twice, from the second-level cache); and
-// any number while its tiles, by the longest sequence the table can hold, are
-// so few that a call's latency decides.
+// rows 175 / 138; one of 100000, 32 rows 141 / 164, 48 rows 200 / 167; one of 2000,
+// 96 rows 23 / 32; 80 tokens alone 18 / 12, after 600 keys 31 / 21; 12 x 20 tokens
+// 30 / 18, 12 x 160 178 / 27; 12 x 20 of 8 heads on one after 600 keys 15 / 30.
+// So: up to 16 rows the first; up to 32 while its units leave SMs free (it reads
+// keys twice, from the second-level cache); and more while its units all find an
+// SM and its tiles, by the longest sequence the table can hold, are so few that
+// a call's latency decides.  Many heads of few rows leave the second one's units
+// as many and nearly empty (12 x 40 tokens, 16 heads of 64: 13 / 19), so up to 48
+// rows then too.
 bool many_rows(const qmv::AttnParams& p, int max_q_len) {
-    const double rows = (double)max_q_len * p.G, sms = qmv::api_sms();
-    const double units = (double)p.n_seqs * p.Hkv * ceil(rows / 16), tiles = (double)p.max_pages * p.page / 64;
+    const double rows = (double)max_q_len * p.G, sms = qmv::api_sms(), heads = (double)p.n_seqs * p.Hkv;
+    const double units = heads * ceil(rows / 16), tiles = (double)p.max_pages * p.page / 64;
     if (rows <= 16 || (rows <= 32 && units <= 2 * sms)) return false;
+    if (units > sms && (rows > 48 || heads <= sms)) return true;
     return units * tiles > 24 * sms;
 }
 
