@@ -199,6 +199,21 @@ def test_many_sequences(q, ws):
     both(q, ws, bt, max_q_len=100)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("new", [[1100, 3], [5, 0, 1030, 64, 90] + [37, 1] * 8, [1, 5, 2, 40] * 45],
+                         ids=["one-long", "20-ragged", "180-ragged"])
+def test_many_units_a_sequence(q, ws, dtype, new):
+    """Sequences of more row tiles than a warp has lanes, in batches that give a
+    sequence 32, a few or one of a block's threads to count them."""
+    kv = [n + 17 * (i % 7) for i, n in enumerate(new)]
+    bt = Batch(new, kv, 8, 1, 64, 16, dtype, seed=len(new))
+    both(q, ws, bt)
+    both(q, ws, bt, window=45)
+    ref = attention64(bt)
+    for hint in (1, 4000):                      # both kernels of the 16-bit types
+        check_attention(bt, *run_attention(q, bt, workspace=ws, max_q_len=hint), ref)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_captured_and_replayed_with_new_lengths(q, ws, dtype):
     """A captured call reads the lengths on the device at each replay."""

@@ -37,8 +37,8 @@
 //
 // Measured (bf16, 32 query and 8 kv heads of 128): 4096 tokens over 16384 keys,
 // causal, 1002 us = 960 TFLOP/s, 58 % of the GEMM burst rate (69 % of the
-// sustained one), tensor pipe 57 % busy: softmax and products wait for each
-// other.  Forms of the same call on the way: one warp that issues both halves'
+// sustained one), tensor pipe and exponential unit each 52 % busy: softmax and
+// products wait for each other.  Forms of the same call on the way: one warp that issues both halves'
 // products 1330 us; tiles of 128 keys 1160; a single S beside P 1190; four warps that
 // copy, one a ring slot, 1136; the scheduling warp 1125; turns at the
 // exponentials 1022; one issuing lane 1005.  A quarter of the exponentials as
