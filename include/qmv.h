@@ -542,7 +542,8 @@ int qmv_kv_append(const void* qkv, long long qkv_stride, const qmv_paged_kv* kv,
  *   lse       [T, n_q_heads] float, or NULL
  *   slopes    [n_q_heads] float (device), or NULL
  *   scale > 0; softcap >= 0; window >= 0; n_q_heads a multiple of n_kv_heads
- *   (scale, softcap and their quotient such that 3 times them is finite);
+ *   (scale, softcap and their quotient such that 3 times them is finite,
+ *   scale / softcap no subnormal);
  *   T * n_q_heads < 2^31 (QMV_EUNSUPPORTED otherwise)
  *   max_q_len the most new tokens of a sequence, 0 if not known: only chooses
  *             the kernel, the result does not depend on it

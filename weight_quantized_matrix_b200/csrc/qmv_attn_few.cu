@@ -213,14 +213,17 @@ __global__ void __launch_bounds__(WARPS * 32, FewGeom<DP, WARPS>::PER_SM) attn_f
             // element (n, 2e + u): row gid + 8 e, key j0 + 8 n + 2 tig + u
             const bool full = j0 >= alo && j0 + 16 <= ahi;
             float mx[2] = {m[0], m[1]};
+            float sc8[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) sc8[x] = sa[x / 4][x % 4] + sb[x / 4][x % 4];
+            if constexpr (MOD) mod.scaled(sc8);
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const int e = x >> 1, j = j0 + 8 * n + 2 * tig + (x & 1);
-                    sa[n][x] += sb[n][x];
-                    if constexpr (MOD) sa[n][x] = mod.apply(sa[n][x], slope[e], j - pos[e]);
-                    else sa[n][x] *= scale2;
+                    if constexpr (MOD) sa[n][x] = fmaf(slope[e], (float)(j - pos[e]), sc8[4 * n + x]);
+                    else sa[n][x] = sc8[4 * n + x] * scale2;
                 }
             if (!full) {
 #pragma unroll

@@ -1,5 +1,6 @@
 // qmv_paged_api.cu -- C entries of the rotary rotation, the append to a paged
 // cache and the attention over it: argument checks and the choice of kernel.
+#include <float.h>
 #include <math.h>
 
 #include <initializer_list>
@@ -221,8 +222,9 @@ int qmv_paged_attention(const void* q, const qmv_paged_kv* kv, void* out, float*
     if (T < 0 || n_q_heads < 1 || n_q_heads % kv->n_kv_heads != 0 || max_q_len < 0) return QMV_EINVAL;
     if ((long long)T * n_q_heads > 0x7FFFFFFF) return QMV_EUNSUPPORTED;
     if (causal != 0 && causal != 1) return QMV_EINVAL;
-    if (window < 0 || !(softcap >= 0.0f) || isinf(softcap) || !(scale > 0.0f) || isinf(scale * qmv::kLog2e)) return QMV_EINVAL;
-    if (softcap > 0.0f && isinf(scale / softcap * (2.0f * qmv::kLog2e))) return QMV_EINVAL;
+    if (window < 0 || !(softcap >= 0.0f) || isinf(softcap * qmv::kLog2e) || !(scale > 0.0f) || isinf(scale * qmv::kLog2e)) return QMV_EINVAL;
+    // a subnormal quotient has too few bits for the scores it is multiplied into
+    if (softcap > 0.0f && (isinf(scale / softcap * (2.0f * qmv::kLog2e)) || scale / softcap < FLT_MIN)) return QMV_EINVAL;
     const int D = kv->head_dim;
     const long long size[2] = {T, n_q_heads}, os[2] = {out_token_stride, out_head_stride};
     if (q_token_stride < 0 || q_head_stride < 0 || !disjoint(D, 2, size, os)) return QMV_EINVAL;
