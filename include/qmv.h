@@ -556,8 +556,8 @@ int qmv_kv_append(const void* qkv, long long qkv_stride, const qmv_paged_kv* kv,
  *             Calls that share a workspace must not overlap on the GPU.
  * Scores, softmax statistics and sums are fp32; out is rounded once.  For f16
  * and bf16 the softmax weights are rounded to the element type before their
- * product with V (off by at most 2^-11 and 2^-8 of each, like out's own
- * rounding).  T == 0 or n_seqs == 0 is a no-op.
+ * product with V (off by at most 2^-11 of each, or 2^-32 of the row's largest, and
+ * 2^-8 of each, like out's own rounding).  T == 0 or n_seqs == 0 is a no-op.
  */
 #define QMV_PAGED_ATTENTION_WORKSPACE_BYTES (40u << 20)
 int qmv_paged_attention(const void* q, const qmv_paged_kv* kv, void* out, float* lse, int T, int n_q_heads,

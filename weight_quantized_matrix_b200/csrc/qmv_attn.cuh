@@ -32,7 +32,7 @@ __device__ __forceinline__ long long key_place(const AttnParams& p, int b, int h
 // 2^-21 is 2^-20 of the result there, with exact limits at both ends.
 template <bool EXACT> struct ScoreMod {
     static constexpr float kBend = 0.7f;
-    float pre, post;            // cap: 1 / c of the scaled score, c log2 e
+    float pre, post;            // scale / c and c log2 e; without a cap scale log2 e
     bool cap;
     __device__ explicit ScoreMod(const AttnParams& p) {
         cap = p.softcap > 0.0f;

@@ -28,7 +28,9 @@
 // 8 in log2 neither the weights (<= 256) nor their fp32 sums can overflow; the
 // output is rescaled in tensor memory, rarely, by the softmax warps themselves.
 // The weights are rounded to the element type for the second product, their
-// sum is not: an error of the size of the output's own rounding.
+// sum is not: an error of the size of the output's own rounding.  For f16 they
+// are taken times 2^7 (2^15 at most, with the slack): those down to 2^-21 of the
+// reference keep all their bits, the rest are off by up to 2^-32 of it.
 //
 // Every wait is bounded (about one second, not counting rows summed again); one
 // that runs out ORs a code into the fault word (1: softmax, 2: copies, 8:
@@ -58,6 +60,7 @@ constexpr int kTile = 64;
 constexpr int kLoaders = 4;                  // warps
 constexpr int kSoftRegs = 176, kOtherRegs = 80;      // 256 x 176 + 256 x 80 = 512 x 128
 constexpr float kSlack = 8.0f;               // log2
+template <class T> constexpr float kUp = __is_same(T, __half) ? 7.0f : 0.0f;     // log2 of what weights are taken times
 
 template <int DP> struct ChunkGeom {
     static constexpr int SLOT = kTile * DP * 2;                 // bytes of a K or V tile
@@ -625,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                 if (ns >= 2 && !warp_wait_all(wait, s_addr(&bars.pv_done[h][u2]), (uint32_t)((ns >> 1) - 1) & 1u)) break;
                 take_turn(&bars.turn[warp & 3]);
                 tc_after();
-                const float base = m == -INFINITY ? 0.0f : m;
+                const float base = m == -INFINITY ? 0.0f : m - kUp<T>;
                 const float2 nb = make_float2(-base, -base), sc2 = make_float2(MOD ? 1.0f : scale2, MOD ? 1.0f : scale2);
                 float2 ls[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
@@ -649,6 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                 if (lane == 0) mbar_arrive1(&bars.p_full[h][u2]);
             }
             if (!wait.ok) break;
+            m -= kUp<T>;                                 // what the weights are relative to, from here on
             // ---- the rows' result ----------------------------------------------
             const bool any = e > a;
             if (any && !warp_wait_all(wait, s_addr(&bars.pv_done[h][(ns - 1) & 1]), (uint32_t)((ns - 1) >> 1) & 1u)) break;
