@@ -60,6 +60,7 @@ constexpr int kTile = 64;
 constexpr int kLoaders = 4;                  // warps
 constexpr int kSoftRegs = 176, kOtherRegs = 80;      // 256 x 176 + 256 x 80 = 512 x 128
 constexpr float kSlack = 8.0f;               // log2
+constexpr float kLarge = 65536.0f;           // references (log2) beyond which rows are summed again
 template <class T> constexpr float kUp = __is_same(T, __half) ? 7.0f : 0.0f;     // log2 of what weights are taken times
 
 template <int DP> struct ChunkGeom {
@@ -152,8 +153,8 @@ __device__ __forceinline__ void give_turn(int* turn) {
 
 // One row over keys [k0, k1) of its sequence, by a warp (lane = dims lane, lane +
 // 32, ..), reading only the keys the row sees: for rows whose sums came out
-// infinite or NaN.  There, and only there, a value that some rows see and others
-// do not may have reached the others through 0 * v.
+// infinite or NaN (there, and only there, a value that some rows see and others
+// do not may have reached the others through 0 * v), and for rows of huge scores.
 template <class T, int DP, bool MOD>
 __device__ __forceinline__ void exact_row(const AttnParams& p, const ScoreMod<false>& mod, int b, int hk, const T* q, int pos,
                                           int k0, int k1, float slope, float (&o)[DP / 32], float& m, float& l) {
@@ -180,7 +181,7 @@ __device__ __forceinline__ void exact_row(const AttnParams& p, const ScoreMod<fa
                 s = fmaf(a.y, x.y, s);
             }
         }
-        s = MOD ? mod.apply(s, slope, j0 + lane - pos) : s * p.scale * kLog2e;
+        s = MOD ? mod.apply(s, slope, j0 + lane - pos) : __fmul_rn(s, p.scale * kLog2e);
         s = !in ? -INFINITY : at < 0 ? NAN : s;
         float mn = s;
 #pragma unroll
@@ -602,10 +603,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                     for (int u = 0; u < 4; ++u) mm[u] = fmaxf(mm[u], x[kTile - 4 + u]);
                     mx = fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3]));
                 }
-                if constexpr (!MOD) mx *= scale2;
+                if constexpr (!MOD) mx = __fmul_rn(mx, scale2);
                 if (mx == -INFINITY || mx != mx) mx = m;
                 // raise the reference when it is left behind by more than the slack
-                const bool raise = mx > m + kSlack || (m == -INFINITY && mx > m);
+                const bool raise = mx - m > kSlack;
                 if (__any_sync(0xFFFFFFFFu, raise)) {
                     const float f = raise ? (m == -INFINITY ? 0.0f : ex2(m - mx)) : 1.0f;
                     if (raise) { m = mx; l *= f; }
@@ -628,8 +629,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                 if (ns >= 2 && !warp_wait_all(wait, s_addr(&bars.pv_done[h][u2]), (uint32_t)((ns >> 1) - 1) & 1u)) break;
                 take_turn(&bars.turn[warp & 3]);
                 tc_after();
-                const float base = m == -INFINITY ? 0.0f : m - kUp<T>;
-                const float2 nb = make_float2(-base, -base), sc2 = make_float2(MOD ? 1.0f : scale2, MOD ? 1.0f : scale2);
+                const float away = m == -INFINITY ? 0.0f : kUp<T> - m;
+                const float2 nb = make_float2(away, away), sc2 = make_float2(MOD ? 1.0f : scale2, MOD ? 1.0f : scale2);
                 float2 ls[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
                 for (int c = 0; c < kTile; c += 32) {
@@ -693,7 +694,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
             } else if (mine && p.lse) {
                 p.lse[row * p.Hq + head] = empty ? -INFINITY : (m + log2f(l)) * kLn2;
             }
-            unsigned again = __ballot_sync(0xFFFFFFFFu, mine && any && odd && !empty);
+            // An FMA does not round its product, as the maximum's was: with references
+            // this large the weights are off by 2^(up to 2^-24 m), all of a row alike,
+            // down to none and up to infinity.  (Rounding the products in the loop
+            // where a warp has such rows cost 1.4 % of every call.)
+            const bool large = !MOD && m != -INFINITY && fabsf(m) > kLarge;
+            unsigned again = __ballot_sync(0xFFFFFFFFu, mine && any && (large || (odd && !empty)));
             if (again && lane == 0) atomicAdd(&bars.busy, 1);      // may take long; it waits for nothing
             const bool busy = again != 0;
 #pragma unroll 1

@@ -87,7 +87,7 @@ __device__ __forceinline__ void f32_weights4(const unsigned char* kb, const floa
         }
     } else {
 #pragma unroll
-        for (int r = 0; r < R; ++r) x[r] *= mod.pre;
+        for (int r = 0; r < R; ++r) x[r] = __fmul_rn(x[r], mod.pre);     // rounded alike for the maximum and the weight
     }
     if (!full) {
 #pragma unroll
@@ -181,7 +181,7 @@ __device__ __forceinline__ void f32_weights(const unsigned char* kb, const float
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             if constexpr (MOD) x[u][r] = mod.apply(x[u][r], rows.slope[rg + 4 * r], j + 4 * u - rows.pos[rg + 4 * r]);
-            else x[u][r] *= mod.pre;
+            else x[u][r] = __fmul_rn(x[u][r], mod.pre);
         }
     if (!full) {
 #pragma unroll

@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(WARPS * 32, FewGeom<DP, WARPS>::PER_SM) attn_f
                 for (int x = 0; x < 4; ++x) {
                     const int e = x >> 1, j = j0 + 8 * n + 2 * tig + (x & 1);
                     if constexpr (MOD) sa[n][x] = fmaf(slope[e], (float)(j - pos[e]), sc8[4 * n + x]);
-                    else sa[n][x] = sc8[4 * n + x] * scale2;
+                    else sa[n][x] = __fmul_rn(sc8[4 * n + x], scale2);     // rounded alike for the maximum and the weight
                 }
             if (!full) {
 #pragma unroll
@@ -257,12 +257,13 @@ __global__ void __launch_bounds__(WARPS * 32, FewGeom<DP, WARPS>::PER_SM) attn_f
                     m[e] = mx[e];
                 }
             }
-            const float base[2] = {m[0] == -INFINITY ? 0.0f : m[0] - kUp, m[1] == -INFINITY ? 0.0f : m[1] - kUp};
+            const float base[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    sa[n][x] = ex2(sa[n][x] - base[x >> 1]);
+                    // (m + 15 is not the same: scores of 2^24 and more would round it)
+                    sa[n][x] = ex2((sa[n][x] - base[x >> 1]) + kUp);
                     l[x >> 1] += sa[n][x];
                 }
             // ---- O += P V -----------------------------------------------------
