@@ -164,10 +164,10 @@ __device__ __forceinline__ void exact_row(const AttnParams& p, const ScoreMod<fa
     m = -INFINITY;
     l = 0.0f;
 #pragma unroll 1
-    for (int j0 = k0; j0 < k1; j0 += 32) {
+    for (unsigned j0 = k0; j0 < (unsigned)k1; j0 += 32) {           // (k1 may be the last int)
         // 32 scores, a key a lane
-        const bool in = j0 + lane < k1;
-        const long long at = in ? key_place(p, b, hk, j0 + lane) : -1;
+        const bool in = j0 + lane < (unsigned)k1;
+        const long long at = in ? key_place(p, b, hk, (int)(j0 + lane)) : -1;
         float s = 0.0f;
 #pragma unroll 2
         for (int c = 0; c < p.D && at >= 0; c += 8) {
@@ -181,7 +181,7 @@ __device__ __forceinline__ void exact_row(const AttnParams& p, const ScoreMod<fa
                 s = fmaf(a.y, x.y, s);
             }
         }
-        s = MOD ? mod.apply(s, slope, j0 + lane - pos) : __fmul_rn(s, p.scale * kLog2e);
+        s = MOD ? mod.apply(s, slope, (int)(j0 + lane - (unsigned)pos)) : __fmul_rn(s, p.scale * kLog2e);
         s = !in ? -INFINITY : at < 0 ? NAN : s;
         float mn = s;
 #pragma unroll
@@ -199,7 +199,7 @@ __device__ __forceinline__ void exact_row(const AttnParams& p, const ScoreMod<fa
         for (int x = 0; x < 32; ++x) {
             const float wx = __shfl_sync(0xFFFFFFFFu, w, x);
             const long long ax = __shfl_sync(0xFFFFFFFFu, at, x);
-            if (j0 + x >= k1) continue;
+            if (j0 + x >= (unsigned)k1) continue;
 #pragma unroll
             for (int i = 0; i < DP / 32; ++i) {
                 const int d = lane + 32 * i;
@@ -446,15 +446,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                         return pg * page16 + (j - e * p.page) * tok16;
                     };
                     // page of this lane's box of a tile, -1 where the tile must go row by row
-                    auto page_of = [&](int j0) -> int {
+                    auto page_of = [&](int tile) -> int {
+                        const int j0 = (int)((unsigned)tile * kTile);      // past the last int: negative, no tile
                         if (lane >= items) return 0;
                         const int e = (j0 + lane / (DP / 64) * g.box_rows) >> g.page_shift;
-                        if (j0 < ulo || j0 + kTile > uhi || e >= p.max_pages) return -1;
+                        if (j0 < ulo || j0 > uhi - kTile || e >= p.max_pages) return -1;
                         const int pg = __ldg(trow + e);
                         return (unsigned)pg < (unsigned)p.n_pages ? pg : -1;
                     };
                     int j = k0 + (((n0 ^ (w >> 1)) & 1));         // this warp's first tile
-                    int pg = items > 0 ? page_of(j * kTile) : -1;
+                    int pg = items > 0 ? page_of(j) : -1;
                     // ---- queries, once the first products of the unit before are done ----
                     flush();
                     if (npiece > 0 && !warp_wait_all(wait, s_addr(&bars.q_empty), (uint32_t)(npiece - 1) & 1u)) break;
@@ -486,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                         if (p.test_skip && blockIdx.x == 0 && w == 0 && fills == 0) {
                             pg = -1;
                         } else if (__all_sync(0xFFFFFFFFu, pg >= 0)) {
-                            const int npg = page_of((j + 2) * kTile);
+                            const int npg = page_of(j + 2);
                             flush();
                             if (!warp_wait_all(wait, empty_a + slot * 8, sph)) break;
                             if (lane == 0) mbar_expect(&bars.kv_full[slot], (uint32_t)Gm::SLOT);
@@ -499,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                             pg = npg;
                         } else {
                             const int at[2] = {place(j * kTile + lane), place(j * kTile + 32 + lane)};
-                            if (items > 0) pg = page_of((j + 2) * kTile);
+                            if (items > 0) pg = page_of(j + 2);
                             // about to wait: what is on its way is reported first
                             if (pend >= 0 && !__all_sync(0xFFFFFFFFu, mbar_test(empty_a + slot * 8, sph))) flush();
                             if (!warp_wait_all(wait, empty_a + slot * 8, sph)) break;
@@ -581,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                 tm_ld32(ts + 32, x + 32);
                 const int j0 = j * kTile;
                 // rows past the unit have queries of zero and need no mask
-                const bool full = __all_sync(0xFFFFFFFFu, r >= nrows || (lo <= j0 && j0 + kTile <= hi));
+                const bool full = __all_sync(0xFFFFFFFFu, r >= nrows || (lo <= j0 && j0 <= hi - kTile));
                 tm_wait_ld();
                 tc_before();
                 __syncwarp();
@@ -708,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
                 again &= again - 1;
                 __syncwarp();
                 auto of = [&](int v) { return __shfl_sync(0xFFFFFFFFu, v, src); };
-                const int sti = of(ti), shead = of(head), spos = of(pos), slo = max(of(lo), a * kTile), shi = min(of(hi), e * kTile);
+                const int sti = of(ti), shead = of(head), spos = of(pos), slo = max(of(lo), a * kTile), shi = (int)min((unsigned)of(hi), (unsigned)e * kTile);
                 const float sslope = __shfl_sync(0xFFFFFFFFu, slope, src);
                 float o[DP / 32], sm2, sl;
                 exact_row<T, DP, MOD>(p, mod, pc->b, pc->h, static_cast<const T*>(p.q) + (long long)(pc->t0 + sti) * p.q_ts + (long long)shead * p.q_hs,

@@ -352,7 +352,7 @@ attn_f32_kernel(const __grid_constant__ AttnParams p, int page_shift) {
         const char* vh = static_cast<const char*>(p.v) + (long long)sc.h * p.head_s * 4;
         const int* trow = p.table + (long long)sc.b * p.max_pages;
         auto place = [&](int t) -> int {
-            const int j = t * Gm::TILE + warp * 16 + (lane & 15);
+            const int j = (int)((unsigned)t * Gm::TILE + warp * 16 + (lane & 15));
             if (t >= k1 || j < ulo || j >= uhi) return -1;
             const int e = page_shift >= 0 ? j >> page_shift : j / p.page;
             if (e >= p.max_pages) return -2;
@@ -458,8 +458,8 @@ attn_f32_kernel(const __grid_constant__ AttnParams p, int page_shift) {
             const unsigned char* vb = kb + 16 * ROWB;
             slot = slot + 1 == STAGES ? 0 : slot + 1;
             const int j0 = t * Gm::TILE + warp * 16;
-            if (j0 >= uhi || j0 + 16 <= ulo) continue;
-            const bool full = j0 >= alo && j0 + 16 <= ahi;
+            if (j0 >= uhi || j0 <= ulo - 16) continue;
+            const bool full = j0 >= alo && j0 <= ahi - 16;
 
             // as many rows as the unit has, in fours
             if (nrows <= 4) f32_step<DP, MOD, 4>(kb, vb, s_q, s_p[warp], s_f[warp], rows, mod, j0, full, o, m, l);

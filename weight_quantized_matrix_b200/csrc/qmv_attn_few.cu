@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(WARPS * 32, FewGeom<DP, WARPS>::PER_SM) attn_f
         // lanes r and r + 16: place of key r of this warp's step t, in units of 16
         // bytes; -1 outside the unit's keys, -2 on a bad page
         auto place = [&](int t) -> int {
-            const int j = t * Gm::TILE + warp * 16 + (lane & 15);
+            const int j = (int)((unsigned)t * Gm::TILE + warp * 16 + (lane & 15));
             if (t >= k1 || j < ulo || j >= uhi) return -1;
             const int e = page_shift >= 0 ? j >> page_shift : j / p.page;
             if (e >= p.max_pages) return -2;
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(WARPS * 32, FewGeom<DP, WARPS>::PER_SM) attn_f
             const uint32_t kb = mine_a + slot * Gm::STEP, vb = kb + 16 * ROWB;
             slot = slot + 1 == STAGES ? 0 : slot + 1;
             const int j0 = t * Gm::TILE + warp * 16;
-            if (j0 >= uhi || j0 + 16 <= ulo) continue;
+            if (j0 >= uhi || j0 <= ulo - 16) continue;
 
             // ---- S = Q K^T: 16 rows x 16 keys ---------------------------------
             float sa[2][4] = {}, sb[2][4] = {};     // two chains of half the dims
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(WARPS * 32, FewGeom<DP, WARPS>::PER_SM) attn_f
                 }
             }
             // element (n, 2e + u): row gid + 8 e, key j0 + 8 n + 2 tig + u
-            const bool full = j0 >= alo && j0 + 16 <= ahi;
+            const bool full = j0 >= alo && j0 <= ahi - 16;
             float mx[2] = {m[0], m[1]};
             float sc8[8];
 #pragma unroll

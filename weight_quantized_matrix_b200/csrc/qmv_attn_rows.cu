@@ -42,13 +42,13 @@ __global__ void __launch_bounds__(kRowWarps * 32) attn_rows_kernel(const __grid_
             o[i] = 0.0f;
         }
         float m = -INFINITY, l = 0.0f;
-        for (int j0 = lo; j0 < hi; j0 += 4) {
+        for (unsigned j0 = lo; j0 < (unsigned)hi; j0 += 4) {          // (hi may be the last int)
             long long at[4];
             float s[4];
             bool bad[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int j = min(j0 + u, hi - 1);
+                const int j = (int)min(j0 + u, (unsigned)hi - 1);
                 at[u] = key_place(p, b, h / p.G, j);
                 bad[u] = at[u] < 0;
                 if (bad[u]) at[u] = 0;
@@ -63,9 +63,9 @@ __global__ void __launch_bounds__(kRowWarps * 32) attn_rows_kernel(const __grid_
             for (int u = 0; u < 4; ++u) {
 #pragma unroll
                 for (int w = 16; w > 0; w >>= 1) s[u] += __shfl_xor_sync(0xFFFFFFFFu, s[u], w);
-                s[u] = mod.apply(s[u], slope, j0 + u - pos);
+                s[u] = mod.apply(s[u], slope, (int)(j0 + u - (unsigned)pos));
                 if (bad[u]) s[u] = NAN;
-                if (j0 + u >= hi) s[u] = -INFINITY;
+                if (j0 + u >= (unsigned)hi) s[u] = -INFINITY;
             }
             float mn = m;
 #pragma unroll
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) attn_rows_kernel(const __grid_
             m = mn;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                if (j0 + u >= hi) break;
+                if (j0 + u >= (unsigned)hi) break;
                 const float w = exp2f(s[u] - base);
                 l += w;
 #pragma unroll
