@@ -488,6 +488,7 @@ int qmv_rope(const void* x, void* y, const int* positions, const float* inv_freq
  *                sequence are not read and their outputs not written
  *   kv_lens      [n_seqs] int32: keys of sequence b, its new tokens included;
  *                new token i is at position kv_lens[b] - n_new + i
+ *   n_seqs       up to 2^30 (QMV_EUNSUPPORTED otherwise)
  * The lists live on the device, so the host cannot check them.  Wrong entries
  * never lead a kernel outside the arrays: see each call.
  */
@@ -544,7 +545,7 @@ int qmv_kv_append(const void* qkv, long long qkv_stride, const qmv_paged_kv* kv,
  *   scale > 0; softcap >= 0; window >= 0; n_q_heads a multiple of n_kv_heads
  *   (scale, softcap and their quotient such that 3 times them is finite,
  *   scale / softcap no subnormal);
- *   T * n_q_heads < 2^31 (QMV_EUNSUPPORTED otherwise)
+ *   T * n_q_heads <= 2^31 - 8449 (QMV_EUNSUPPORTED otherwise)
  *   max_q_len the most new tokens of a sequence, 0 if not known: only chooses
  *             the kernel, the result does not depend on it
  *   workspace NULL, or a device buffer of QMV_PAGED_ATTENTION_WORKSPACE_BYTES,

@@ -65,6 +65,7 @@ __device__ __forceinline__ int unit_tiles(const AttnParams& p, const SeqInfo& s,
 }
 
 constexpr int kAlignTiles = 64;         // parts up to this many tiles end with their units
+constexpr long long kMostTiles = 1LL << 26;     // of a unit: 2^31 keys in tiles of 32
 
 struct SchedSmem {
     long long warp_sum[32];
@@ -75,7 +76,8 @@ struct SchedSmem {
 
 // One block's walk over its part.  Work is counted in chunks of Q key tiles of a
 // unit (its last chunk may be shorter): Q = 1 unless parts are to end with their
-// units, or there are more tiles than an int counts.
+// units, or there are 2^30 tiles or more.  (Tiles are counted in 64 bits, chunks
+// fit an int.)
 template <int ROWS, int TK> struct Sched {
     int W, w0, w1;          // all chunks, this block's part
     int q, rem;             // W = nblk q + rem: the first rem blocks take q + 1 chunks
@@ -126,7 +128,7 @@ template <int ROWS, int TK> struct Sched {
         const int rounds = (p.n_seqs + seqs - 1) >> (__ffs(seqs) - 1);
         int kept = -2;          // tiles of the lane's only unit, -1 for none, in the one round; -2: not known
         auto cost = [&](int bb) {
-            int v = 0;
+            long long v = 0;
             if (kept >= -1) {
                 if (kept >= 0) v = chunks(kept);
             } else if (bb < p.n_seqs) {
@@ -149,8 +151,8 @@ template <int ROWS, int TK> struct Sched {
             return v;
         };
         // inclusive scan over the block (the value counts once a sequence)
-        auto scan = [&](int c1, long long& total) {
-            long long v = sub == 0 ? (long long)c1 * p.Hkv : 0;
+        auto scan = [&](long long c1, long long& total) {
+            long long v = sub == 0 ? c1 * p.Hkv : 0;
 #pragma unroll
             for (int w = 1; w < 32; w <<= 1) {
                 const long long u = __shfl_up_sync(0xFFFFFFFFu, v, w);
@@ -172,7 +174,8 @@ template <int ROWS, int TK> struct Sched {
         split = p.partials != nullptr;
         live = false;
         Q = 1;
-        int v = 0, pass = 0;    // 0: count tiles, 1, 2: parts of each, 5/4 each tiles end with their units, 3: they do not
+        long long v = 0;
+        int pass = 0;           // 0: count tiles, 1, 2: parts of each, 5/4 each tiles end with their units, 3: they do not
         int each = 0;           // tiles a block
         long long incl = 0, all;
 #pragma unroll 1
@@ -186,9 +189,9 @@ template <int ROWS, int TK> struct Sched {
                 all += total;
             }
             if (pass == 0) {
-                if (all == 0) return;
+                if (all <= 0) return;
                 if (all >> 30) {
-                    Q = (int)(all >> 29) + 1;
+                    Q = (int)min(all >> 29, kMostTiles) + 1;
                     pass = 3;
                     continue;
                 }
@@ -201,6 +204,12 @@ template <int ROWS, int TK> struct Sched {
             } else if (pass < 3 && all > (long long)gridDim.x) {
                 ++pass;
                 Q = pass == 3 ? max(4, each / 8) : max(min_tiles, each * 5 / 4);
+                continue;
+            } else if (all >> 31) {
+                // many units of one chunk: an int holds those of all rows there can
+                // be; more are lists that do not ascend, which nothing is run for
+                if (Q > kMostTiles) return;
+                Q = (int)min(Q * 8LL, kMostTiles + 1);
                 continue;
             }
             break;
@@ -220,11 +229,11 @@ template <int ROWS, int TK> struct Sched {
                 v = cost(r * seqs + (tid >> lg));
                 incl = scan(v, total);
             }
-            const long long end = base + incl, beg = end - (long long)v * p.Hkv;
+            const long long end = base + incl, beg = end - v * p.Hkv;
             if (sub == 0 && beg <= w0 && w0 < end) {
                 sm.seq = r * seqs + (tid >> lg);
                 sm.seq_at = beg;
-                sm.per_head = v;
+                sm.per_head = (int)v;
             }
             base += total;
             if (base > w0) break;       // the same for every thread

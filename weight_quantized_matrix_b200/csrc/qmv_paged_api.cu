@@ -53,7 +53,7 @@ int check_cache(const qmv_paged_kv* kv) {
     if (kv->n_pages < 1 || kv->page_size < 1 || kv->n_kv_heads < 1 || kv->head_dim < 1 || kv->n_seqs < 0 ||
         kv->max_pages < 1)
         return QMV_EINVAL;
-    if (kv->head_dim > QMV_MAX_HEAD_DIM) return QMV_EUNSUPPORTED;
+    if (kv->head_dim > QMV_MAX_HEAD_DIM || kv->n_seqs > (1 << 30)) return QMV_EUNSUPPORTED;
     const long long size[3] = {kv->n_pages, kv->page_size, kv->n_kv_heads};
     const long long stride[3] = {kv->page_stride, kv->token_stride, kv->head_stride};
     if (!disjoint(kv->head_dim, 3, size, stride)) return QMV_EINVAL;
@@ -220,7 +220,8 @@ int qmv_paged_attention(const void* q, const qmv_paged_kv* kv, void* out, float*
     int st = check_cache(kv);
     if (st != QMV_OK) return st;
     if (T < 0 || n_q_heads < 1 || n_q_heads % kv->n_kv_heads != 0 || max_q_len < 0) return QMV_EINVAL;
-    if ((long long)T * n_q_heads > 0x7FFFFFFF) return QMV_EUNSUPPORTED;
+    // row counts are rounded up to a step of 32 tiles of 256 rows in an int
+    if ((long long)T * n_q_heads > 0x7FFFFFFF - 33 * 256) return QMV_EUNSUPPORTED;
     if (causal != 0 && causal != 1) return QMV_EINVAL;
     if (window < 0 || !(softcap >= 0.0f) || isinf(softcap * qmv::kLog2e) || !(scale > 0.0f) || isinf(scale * qmv::kLog2e)) return QMV_EINVAL;
     // a subnormal quotient has too few bits for the scores it is multiplied into
