@@ -3,7 +3,8 @@ from __future__ import annotations
 
 import pytest
 
-from test_paged_abi import EINVAL, EUNSUP, append, attention
+import weight_quantized_matrix_b200 as q
+from test_paged_abi import A, EINVAL, EUNSUP, append, attention
 
 
 def test_caps_whose_quotient_has_too_few_bits():
@@ -25,3 +26,36 @@ def test_row_counts_that_an_int_cannot_round_up():
 def test_more_sequences_than_are_counted(call):
     assert call(T=0, n_seqs=2 ** 30) == 0
     assert call(T=0, n_seqs=2 ** 30 + 1) == EUNSUP and call(n_seqs=2 ** 31 - 1) == EUNSUP
+
+
+class FakeTensor:
+    """What the binding asks a tensor for."""
+
+    def __init__(self, nbytes, whole=True, device=0):
+        self.nbytes, self.whole, self.device = nbytes, whole, device
+
+    def data_ptr(self):
+        return A
+
+    def get_device(self):
+        return self.device
+
+    def is_contiguous(self):
+        return self.whole
+
+
+def test_a_workspace_tensor_that_is_too_small():
+    """The kernels write all of the workspace's bytes."""
+    size = q.PAGED_ATTENTION_WORKSPACE_BYTES
+    assert attention(T=0, ws=FakeTensor(size)) == 0 and attention(T=0, ws=FakeTensor(size + 4096)) == 0
+    for ws in (FakeTensor(size - 1), FakeTensor(0), FakeTensor(1 << 20), FakeTensor(size, whole=False)):
+        assert attention(ws=ws) == EINVAL and attention(T=0, ws=ws) == EINVAL
+    assert attention(T=0, ws=A) == 0                        # an address: the caller's word
+
+
+def test_the_workspace_of_the_header():
+    import pathlib
+    import re
+    text = (pathlib.Path(q.__file__).parents[1] / "include" / "qmv.h").read_text()
+    m = re.search(r"#define QMV_PAGED_ATTENTION_WORKSPACE_BYTES \((\d+)u << (\d+)\)", text)
+    assert int(m[1]) << int(m[2]) == q.PAGED_ATTENTION_WORKSPACE_BYTES

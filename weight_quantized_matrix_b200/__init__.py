@@ -410,7 +410,8 @@ def qmv_paged_attention(q, k_cache, v_cache, page_table, q_starts, kv_lens, out,
     [T, n_q_heads] float32.  cache_strides as in qmv_kv_append; q_strides and
     out_strides are (token, head) in elements.  workspace: None, or a
     zero-filled device buffer of PAGED_ATTENTION_WORKSPACE_BYTES bytes that
-    every call leaves ready for the next."""
+    every call leaves ready for the next (a tensor that is smaller, or not
+    contiguous, is refused)."""
     cs = cache_strides or (page_size * n_kv_heads * head_dim, n_kv_heads * head_dim, head_dim)
     qs = q_strides or (n_q_heads * head_dim, head_dim)
     os_ = out_strides or (n_q_heads * head_dim, head_dim)

@@ -47,7 +47,7 @@ static int as_float(PyObject* o, float* out) {
 /* An array argument of the calls below: None, an int (a device address), or a
  * tensor, of which data_ptr() is taken.  A tensor that is not on device `dev` (-1:
  * not known) or not on a CUDA device at all sets *elsewhere. */
-static PyObject *s_data_ptr, *s_get_device;
+static PyObject *s_data_ptr, *s_get_device, *s_nbytes, *s_is_contiguous;
 static int as_array(PyObject* o, int dev, void** out, int* elsewhere) {
     if (o == Py_None || PyLong_Check(o)) return as_ptr(o, out);
     PyObject* r = PyObject_CallMethodNoArgs(o, s_data_ptr);
@@ -62,6 +62,23 @@ static int as_array(PyObject* o, int dev, void** out, int* elsewhere) {
     if (d == -1 && PyErr_Occurred()) return -1;
     if (d < 0 || (dev >= 0 && d != dev)) *elsewhere = 1;
     return 0;
+}
+
+/* Whether a tensor does not hold `bytes` bytes in one piece: 1, 0, or -1 on an
+ * error.  Addresses and None: 0, their size is not known. */
+static int as_too_small(PyObject* o, long long bytes) {
+    if (o == Py_None || PyLong_Check(o)) return 0;
+    PyObject* r = PyObject_GetAttr(o, s_nbytes);
+    if (!r) return -1;
+    const long long has = PyLong_AsLongLong(r);
+    Py_DECREF(r);
+    if (has == -1 && PyErr_Occurred()) return -1;
+    if (has < bytes) return 1;
+    r = PyObject_CallMethodNoArgs(o, s_is_contiguous);
+    if (!r) return -1;
+    const int whole = PyObject_IsTrue(r);
+    Py_DECREF(r);
+    return whole < 0 ? -1 : !whole;
 }
 
 /* affine(x, w, scales, biases, y, M, N, K, bits, group, dtype, batch, x_batched, stream) -> status */
@@ -199,7 +216,9 @@ static PyObject* py_paged_attention(PyObject* self, PyObject* const* a, Py_ssize
     for (int i = 0; i < 4; ++i) if (as_ll(a[25 + i], &s[i])) return NULL;
     for (int i = 0; i < 2; ++i) if (as_float(a[29 + i], &f[i])) return NULL;
     if (as_ptr(a[31], &st)) return NULL;
-    if (elsewhere) return PyLong_FromLong(QMV_EINVAL);
+    const int small = as_too_small(a[19], QMV_PAGED_ATTENTION_WORKSPACE_BYTES);
+    if (small < 0) return NULL;
+    if (elsewhere || small) return PyLong_FromLong(QMV_EINVAL);
     int r;
     Py_BEGIN_ALLOW_THREADS
     r = qmv_paged_attention(p[0], &kv, p[1], (float*)p[2], v[0], v[1], f[0], v[2], v[3], f[1], (const float*)p[3],
@@ -223,6 +242,8 @@ static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_qmv_fast", NULL, -1
 PyMODINIT_FUNC PyInit__qmv_fast(void) {
     s_data_ptr = PyUnicode_InternFromString("data_ptr");
     s_get_device = PyUnicode_InternFromString("get_device");
-    if (!s_data_ptr || !s_get_device) return NULL;
+    s_nbytes = PyUnicode_InternFromString("nbytes");
+    s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
+    if (!s_data_ptr || !s_get_device || !s_nbytes || !s_is_contiguous) return NULL;
     return PyModule_Create(&module);
 }
