@@ -796,6 +796,7 @@ namespace qmv {
 int api_finish(cudaError_t e) { return finish(e); }
 int api_sms() { return device_sms(); }
 unsigned* api_fault_word() { return fault_word(); }
+bool api_pdl();
 int api_test_skip() { return g_test_skip.load(std::memory_order_relaxed); }
 bool api_encode_pages(CUtensorMap* m, const void* base, bool f16, int D, int page, int heads, int pages, long long tok_s,
                       long long head_s, long long page_s, int rows);
@@ -811,6 +812,12 @@ bool pdl_enabled() {
     }
     return v == 1;
 }
+
+}  // namespace
+
+bool qmv::api_pdl() { return pdl_enabled(); }
+
+namespace {
 
 int check_common(const void* x, const void* w, const void* s, void* y, int M, int N, int K, int dtype) {
     if (M < 0 || N < 0 || K < 0) return QMV_EINVAL;

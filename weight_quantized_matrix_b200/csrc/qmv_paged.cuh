@@ -17,6 +17,7 @@ namespace qmv {
 int api_finish(cudaError_t e);      // QMV_OK, or QMV_ECUDA (recorded for qmv_last_cuda_error)
 int api_sms();                      // multiprocessors of the current device
 unsigned* api_fault_word();         // fault word of the current device, null if unknown
+bool api_pdl();                     // programmatic dependent launch (off with QMV_PDL=0)
 int api_test_skip();                // whether qmv_test_skip_last_copy is on
 bool api_encode_pages(CUtensorMap* m, const void* base, bool f16, int D, int page, int heads, int pages, long long tok_s,
                       long long head_s, long long page_s, int rows);
@@ -120,7 +121,8 @@ inline cudaError_t allow_smem(Kern kern, std::atomic<unsigned>& configured, int 
 }
 
 // Launch with programmatic dependent launch: the kernel may begin while the
-// kernel before it drains, and waits for it before it touches memory.
+// kernel before it drains, and waits for it before it touches memory.  Without it
+// (api_pdl) the kernel's wait returns at once.
 template <class Kern, class... Args>
 inline cudaError_t launch_dependent(Kern kern, dim3 grid, dim3 block, size_t smem, cudaStream_t st, const Args&... args) {
     cudaLaunchConfig_t cfg = {};
@@ -132,7 +134,7 @@ inline cudaError_t launch_dependent(Kern kern, dim3 grid, dim3 block, size_t sme
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = api_pdl() ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
