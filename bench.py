@@ -46,6 +46,9 @@ over ranks.  nvidia-smi clocks are sampled (20 ms) from the graph warm-up throug
 the timed region.  The per-shape lines (and the roofline's dominant kernel)
 come from a second pass that replays each shape's own graph alone, L2 flushed,
 between a pair of CUDA events (one graph launch per shape included).
+The result line holds the workload's own shapes in full and the other sets' as
+[shape, us per call, fraction of the HBM peak]; those sets' full lines go to
+stderr, one JSON object a line.
 
 --impl reference times the fp64 CPU oracle (the only other implementation of
 this operation there is) on a bounded sample of the same workload, on the host
@@ -691,6 +694,16 @@ def alu_roof(flops, us, alu_peak):
     return {"alu_tflops": round(tf, 2), "alu_frac": round(tf / alu_peak, 4)}
 
 
+def short_lines(lines):
+    """The shape lines as {set: [[shape, us_per_call, frac_of_hbm], ...]}: the whole
+    lines, launch plans and spreads included, go to stderr, since with more than
+    a hundred of them the result line had 46 KB and was not read back."""
+    sets = {}
+    for line in lines:
+        sets.setdefault(line["set"], []).append([line["shape"], line["us_per_call"], line["frac_of_hbm"]])
+    return sets
+
+
 def shape_lines(q, torch, dev, stream, flush, flush_rd, peak, sets=None, alu_peak=None):
     """Throughput per format, bits and shape (the metric's breakdown), each
     line from ONE CUDA graph of R calls back to back on R weight copies that
@@ -969,7 +982,11 @@ def run_ours(args, rank, world, local_rank):
     }
     if args.workload == "chain8" and not args.no_shapes:
         # the metric's breakdown per format / bits / shape; not part of `value`
-        out["shapes"] += shape_lines(q, torch, dev, stream, flush, flush_rd, peak, args.sets, alu_peak)
+        more = shape_lines(q, torch, dev, stream, flush, flush_rd, peak, args.sets, alu_peak)
+        out["sets"] = short_lines(more)
+        if rank == 0:
+            for line in more:
+                print(json.dumps(line), file=sys.stderr, flush=True)
     if rank == 0:
         out["cpu_baseline"] = (cpu_baseline(args.workload) if not args.no_cpu_baseline
                                else {"value": None, "unit": "us/call", "kind": "oracle",
