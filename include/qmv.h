@@ -484,8 +484,8 @@ int qmv_rope(const void* x, void* y, const int* positions, const float* inv_freq
  *                e * page_size .. of sequence b at [b, e]
  *   q_starts     [n_seqs + 1] int32, ascending: sequence b's new tokens are
  *                rows q_starts[b] .. q_starts[b + 1] - 1 of the call's T rows
- *                (none is allowed); rows before the first and behind the last
- *                sequence are not read and their outputs not written
+ *                (none is allowed); what rows before the first and behind the
+ *                last sequence hold has no effect, their outputs are not written
  *   kv_lens      [n_seqs] int32: keys of sequence b, its new tokens included;
  *                new token i is at position kv_lens[b] - n_new + i
  *   n_seqs       up to 2^30 (QMV_EUNSUPPORTED otherwise)
@@ -546,15 +546,25 @@ int qmv_kv_append(const void* qkv, long long qkv_stride, const qmv_paged_kv* kv,
  *   (scale, softcap and their quotient such that 3 times them is finite,
  *   scale / softcap no subnormal);
  *   T * n_q_heads <= 2^31 - 8449 (QMV_EUNSUPPORTED otherwise)
- *   max_q_len the most new tokens of a sequence, 0 if not known: only chooses
- *             the kernel, the result does not depend on it
+ *   max_q_len the most new tokens of a sequence, 0 if not known (T is taken
+ *             then).  Any value is right: it chooses the kernel and the width of
+ *             its steps, and with them the order of the sums and how the softmax
+ *             weights round.  Without it a batch of one-token sequences runs on
+ *             the kernel for many rows (64 of them: 1.4 times as long).
  *   workspace NULL, or a device buffer of QMV_PAGED_ATTENTION_WORKSPACE_BYTES,
  *             16-byte aligned, ALL ZERO before its first use (cudaMemset
  *             once); every call leaves it ready for the next, of any sizes.
  *             With it the keys of a sequence are shared out over blocks
  *             (which the sums' order depends on, so results without it may
  *             differ by rounding; with the same arguments they do not).
+ *             Without it each sequence and kv head is one block's (one token
+ *             over 131001 keys: 8 times as long).
  *             Calls that share a workspace must not overlap on the GPU.
+ * Keys and values are streamed where head_dim, the q and cache strides and the
+ * q, k and v addresses are multiples of 16 bytes and the last page of a tensor
+ * begins within 32 GiB of its first.  Any other layout is right too, by a kernel
+ * of one warp a row, which is tens of times slower.  16-bit heads of more than 128
+ * dims run the kernel for few rows whatever max_q_len is.
  * Scores, softmax statistics and sums are fp32; out is rounded once.  For f16
  * and bf16 the softmax weights are rounded to the element type before their
  * product with V (off by at most 2^-11 of each, or 2^-32 of the row's largest, and

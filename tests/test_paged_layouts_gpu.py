@@ -81,3 +81,27 @@ def test_pages_far_apart(q, ws, dtype, beyond):
                                         max_q_len=max(new)), ref)
         del pool
         torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype,D", [(t, d) for t in ("bf16", "f16") for d in (8, 24, 40, 72, 104, 120, 136, 200, 248)]
+                         + [("f32", d) for d in (4, 12, 36, 68, 100, 132, 252)])
+def test_every_padding_of_the_heads(q, ws, dtype, D):
+    """Heads of whole 16 bytes that fill 64, 128 or 256 dims only in part; the
+    output by odd strides inside rows whose rest stays as it is."""
+    for new, kv in (([1, 2], [90, 33]), ([70, 5], [150, 64])):
+        bt = Batch(new, kv, 6, 2, D, 16, dtype, seed=D)
+        ref = attention64(bt)
+        k, v, qd = bt.cache(bt.k), bt.cache(bt.v), bt.q.cuda()
+        head, row = D + 3, 6 * (D + 3) + 5
+        for table in (bt.table, wide_table(bt)):
+            for w in (ws, None):
+                buf = torch.full((bt.T * row + 1,), 7.0, dtype=TORCH_DT[dtype], device="cuda")
+                lse = torch.full((bt.T, 6), 7.0, dtype=torch.float32, device="cuda")
+                q.qmv_paged_attention(qd, k, v, table.cuda(), bt.starts.cuda(), bt.lens.cuda(), buf[1:], lse, bt.T, 6, 2, D,
+                                      2, bt.n_pages, 16, table.shape[1], 1 / math.sqrt(D), dtype, cache_strides=bt.strides,
+                                      out_strides=(row, head), max_q_len=max(new), workspace=w)
+                torch.cuda.synchronize()
+                got = buf[1:].view(bt.T, row)
+                heads = got[:, :6 * head].reshape(bt.T, 6, head)
+                check_attention(bt, heads[..., :D], lse, ref)
+                assert (heads[..., D:] == 7).all() and (got[:, 6 * head:] == 7).all() and float(buf[0]) == 7

@@ -28,7 +28,8 @@
 // 8 in log2 neither the weights (<= 256) nor their fp32 sums can overflow; the
 // output is rescaled in tensor memory, rarely, by the softmax warps themselves.
 // The weights are rounded to the element type for the second product, their
-// sum is not: an error of the size of the output's own rounding.  For f16 they
+// sum is not: an error of the size of the output's own rounding (the largest
+// weight among them, since the reference may lie below it).  For f16 they
 // are taken times 2^7 (2^15 at most, with the slack): those down to 2^-21 of the
 // reference keep all their bits, the rest are off by up to 2^-32 of it.
 //
@@ -38,7 +39,7 @@
 // block frees its tensor memory and ends.
 //
 // Measured (bf16, 32 query and 8 kv heads of 128): 4096 tokens over 16384 keys,
-// causal, 1002 us = 960 TFLOP/s, 58 % of the GEMM burst rate (69 % of the
+// causal, 1000 us = 960 TFLOP/s, 58 % of the GEMM burst rate (69 % of the
 // sustained one), tensor pipe and exponential unit each 52 % busy: softmax and
 // products wait for each other.  Forms of the same call on the way: one warp that issues both halves'
 // products 1330 us; tiles of 128 keys 1160; a single S beside P 1190; four warps that
@@ -405,9 +406,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
             __syncwarp();
         } else if (warp >= kThreads / 32 - kLoaders) {
             // -------------------------------------------------- the copies ----
-            // Slot x of the ring is filled by warp x % 4 alone: a warp's K or V, every
-            // second tile.  (All four warps on each tile took 1000 clocks a slot,
-            // the time of one warp's instructions, and bound the kernel.)
+            // Item x in the order of the ring (K and V of a tile in turn) is filled by
+            // warp x % 4 alone: a warp's K or V, every second tile.  (All four warps on
+            // each tile took 1000 clocks a slot, the time of one warp's instructions,
+            // and bound the kernel.)
             Waiter wait{&bars, p.fault, 2u, true};
             const int w = warp - (kThreads / 32 - kLoaders), kv = w & 1;
             const int chunks = p.D / 8;

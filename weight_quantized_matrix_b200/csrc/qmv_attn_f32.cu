@@ -16,8 +16,9 @@
 // Measured: 12 sequences of 2-5 new tokens over 100-2100 keys, 16 heads of 64: 43 us =
 // 2.8 TB/s; one token of 8 sequences over 4000 keys, 8 kv heads of 128, 74 us = 3.5 TB/s:
 // bound by the latency of a step's instructions, at one or two warps a scheduler.
-// 1000 tokens over 2000 keys, 32 heads of 128: 1127 us = 22 TFLOP/s, so bound, too
-// (FMA pipe 35 % busy); 1290 with a lane a key and all rows.
+// 1000 tokens over 2000 keys, 32 heads of 128: 1140 us = 22 TFLOP/s, so bound, too
+// (issue slots 32 % busy); 1290 with a lane a key and all rows.  At 256 dims the
+// kernel spills 326 bytes a thread.
 #include <algorithm>
 
 #include "qmv_attn_mma.cuh"

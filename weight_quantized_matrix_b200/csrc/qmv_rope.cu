@@ -6,11 +6,12 @@
 // p has up to 31 bits and inv_freq 24, so an fp32 product loses the angle of a
 // far position; the product and its reduction to a fraction of one turn are
 // done in fp64 and only that fraction, in [-1/2, 1/2], is rounded to fp32 for
-// sincospif (angle error below 2^-24 turns).  The rotation itself is fp32, rounded
+// sincospif (angle error below 2^-24 turns up to angles of 2^29, 2^-23 at the last
+// int; that is fp64's own rounding).  The rotation itself is fp32, rounded
 // once to the element type.
 //
 // Memory-bound: every element is read once and written once.  A block takes
-// `tpb` tokens (as many as give its 256 threads two items each); its threads
+// `tpb` tokens (as many as give its 256 threads up to three items each); its threads
 // first load their vectors, then look the tokens up and share out their cosines
 // and sines through shared memory (one evaluation per token and pair, for all
 // heads), then rotate and store.  A work item is the pair of vectors a rotation mixes:
