@@ -536,8 +536,9 @@ int qmv_kv_append(const void* qkv, long long qkv_stride, const qmv_paged_kv* kv,
  *     out = sum_j softmax(s)_j v_j,   lse = log sum_j exp(s_j)
  * A row that sees no key, or whose scores are all -infinity, gives out = 0
  * and lse = -infinity.  Keys and values a row does not see never reach it,
- * whatever they hold.  A key that lies on a bad page (see qmv_kv_append) makes
- * the rows that see it NaN.
+ * whatever they hold.  An infinite value makes the rows that see it infinite, or
+ * NaN where its weight is below what its type holds.  A key that lies on a bad
+ * page (see qmv_kv_append) makes the rows that see it NaN.
  *   q, out    [T, n_q_heads, head_dim] dtype of the cache, by token and head
  *             strides (elements; q's may be 0); out must not overlap q or the cache
  *   lse       [T, n_q_heads] float, or NULL
